@@ -99,6 +99,117 @@ KIMODO_API int kimodo_layernorm(const float* y, void* out, int out_bf16, const f
 KIMODO_API int kimodo_global_to_local_root(const float* root, const float* x, const int* lengths, int batch,
                                            int frames, float* body_in, void* stream);
 
+/* ------------------------------------------------------------------ 8-bit projections
+ *
+ * A projection in 8-bit integers: its input rows are quantised with one scale each
+ * (kimodo_rms_norm_int8 or kimodo_quantize_int8), its weight matrix once with one scale per
+ * output channel (kimodo_quantize_int8 on its rows), and kimodo_gemm_int8 multiplies them.
+ * No counterpart is on the pages; the calls stand beside kimodo_layernorm and
+ * kimodo_gemm_bf16.  Every tensor must be memory of the current device (else
+ * KIMODO_EINVAL).  All calls may be captured into a CUDA graph; make one call of a kind
+ * before the capture, so that its kernels are loaded.
+ */
+
+/*
+ * Rows in 8-bit integers: scale[r] = max_c |x[r, c]| / 127, q[r, c] = rint(127 x[r, c] /
+ * max_c |x[r, c]|) (ties to even), so x is about q * scale.  A row of zeros has q = 0,
+ * scale = 0; a row with a NaN or an infinity has q = 0 and scale NaN.
+ * x: fp32 (x_bf16 = 0) or bf16 (1) [rows, cols], row stride ldx elements.  q: int8, row
+ * stride ldq.  scale: fp32 [rows].  1 <= rows, 1 <= cols <= 32768.  Rows on 16-byte
+ * boundaries (8 for q) with cols a multiple of 8 take the faster path; none is required.
+ */
+KIMODO_API int kimodo_quantize_int8(const void* x, long long ldx, int x_bf16, void* q, long long ldq,
+                                    float* scale, int rows, int cols, void* stream);
+
+/*
+ * RMS norm with the residual's addition, its output in 8-bit integers:
+ *   h = x + resid (fp32; resid NULL: h = x), resid_out = h in the residual's type,
+ *   t = h gamma / sqrt(mean_c h^2 + eps), q and scale as kimodo_quantize_int8 of t.
+ * t is taken from the fp32 sum, not from the rounded resid_out.
+ * x as above; resid, resid_out: fp32 (resid_bf16 = 0) or bf16 (1), strides ldr, ldro; both
+ * or neither; resid_out may equal resid (in place, same stride) but not overlap it or x
+ * otherwise.  gamma: fp32 [cols].  eps: finite, >= 0.
+ */
+KIMODO_API int kimodo_rms_norm_int8(const void* x, long long ldx, int x_bf16, const void* resid, long long ldr,
+                                    void* resid_out, long long ldro, int resid_bf16, const float* gamma, float eps,
+                                    void* q, long long ldq, float* scale, int rows, int cols, void* stream);
+
+/*
+ * Product in 8-bit integers on the tcgen05 tensor cores:
+ *   out[m, n] = epilogue(a_scale[m] w_scale[n] sum_k A[m, k] W[n, k] + bias[n]).
+ * The sum is exact (32-bit integers): results do not depend on how the work is split.
+ * A: int8 [M, K], row stride lda; W: int8 [N, K], row stride ldw; both 16-byte aligned with
+ * lda, ldw multiples of 16 (columns past K are not read into the sum).  1 <= K <=
+ * KIMODO_INT8_MAX_K, the largest K whose sum cannot leave 32 bits.
+ * a_scale: fp32 [M]; w_scale: fp32 [N]; bias: fp32 [N] or NULL.
+ * epilogue: KIMODO_EPI_*; resid fp32 [M, ldr] with KIMODO_EPI_BIAS_RESID (may equal out),
+ * ignored otherwise.  out: bf16 (out_f32 = 0) or fp32 (1), row stride ldo, no alignment
+ * beyond its elements; GELU and SiLU write bf16, the residual epilogue fp32.
+ */
+#define KIMODO_INT8_MAX_K 131071
+KIMODO_API int kimodo_gemm_int8(const void* A, long long lda, const float* a_scale, const void* W, long long ldw,
+                                const float* w_scale, const float* bias, const float* resid, long long ldr,
+                                void* out, long long ldo, int M, int N, int K, int epilogue, int out_f32,
+                                void* stream);
+
+/* ------------------------------------------------------------------ attention with scored masks
+ *
+ * kimodo_attention_* with other head layouts, lengths, score forms and masks.  Query i of
+ * sequence b has position p_i = q_start[b] + i; for query head h and key j:
+ *   x_ij = scale q_i . k_j
+ *   x_ij = cap tanh(x_ij / cap)          if cap > 0
+ *   x_ij = x_ij - slopes[h] |p_i - j|    if slopes
+ * Key j is seen if j < kv_lengths[b], and, with causal, j <= p_i or j < prefix[b], and, with
+ * documents, q_documents[b, i] == kv_documents[b, j] >= 0 (a negative number: in no
+ * document).  o_i = sum_j softmax_j(x_ij) v_j over the keys seen, 0 if there are none.
+ * NaN and infinities in keys and values that a query does not see never reach its output.
+ *
+ * q, out: [batch, q_len, q_heads, head_dim]; k, v: [batch, kv_len, kv_heads, head_dim]; head
+ *   h reads key head h / (q_heads / kv_heads).  head_dim 64 or 128, its elements
+ *   consecutive.  Strides (elements) of batch, token and head: multiples of 16 bytes, at
+ *   least head_dim; that of an extent of one is ignored.  Bases 16-byte aligned.  out must
+ *   not overlap the inputs.
+ * dtype: KIMODO_BF16 (tcgen05 tensor cores; fp32 scores, softmax and sums) or KIMODO_FP32.
+ * slopes: fp32 [q_heads].  prefix (with causal), kv_lengths, q_start: int32 [batch];
+ *   q_documents int32 [batch, q_len], kv_documents int32 [batch, kv_len] (both or
+ *   neither).  NULL switches an option off; kv_lengths NULL: kv_len (lengths are clamped to
+ *   [0, kv_len]); q_start NULL: kv_len - q_len (the queries are the last tokens).
+ *   Positions must stay within +-2^30.
+ * 1 <= batch, q_len; 0 <= kv_len; q_len, kv_len <= KIMODO_MAX_KEYS.
+ * workspace: device memory of at least the bytes that kimodo_attention_scored_workspace
+ *   gives for the same sizes (0 for most), 16-byte aligned, the caller's until the call's
+ *   work is done; calls that may overlap (streams, captured graphs) need their own.
+ */
+#define KIMODO_MAX_KEYS 16777216
+typedef struct kimodo_scored_attention {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  const float* slopes;
+  const int* prefix;
+  const int* q_documents;
+  const int* kv_documents;
+  const int* kv_lengths;
+  const int* q_start;
+  long long q_strides[3]; /* batch, token, head */
+  long long k_strides[3];
+  long long v_strides[3];
+  long long out_strides[3];
+  int batch, q_len, kv_len, q_heads, kv_heads, head_dim;
+  int dtype;
+  int causal;
+  float scale;
+  float cap;
+} kimodo_scored_attention;
+KIMODO_API int kimodo_attention_scored_workspace(const kimodo_scored_attention* args, size_t* bytes);
+KIMODO_API int kimodo_attention_scored(const kimodo_scored_attention* args, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* Synchronise `stream` and report (and clear) a bounded wait that ran out in a kernel-level
+ * call on the current device since the last check (KIMODO_ETIMEOUT). */
+KIMODO_API int kimodo_kernel_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif

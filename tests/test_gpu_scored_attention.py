@@ -1,0 +1,212 @@
+"""Attention with scored masks against its definition in 64 bits."""
+import pytest
+import torch
+
+import transformer_denoiser_b200 as kb
+from gpu_fixtures import require_cuda
+from operator_refs import check_attention
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _fp32_default():
+    """Tensors drawn here are fp32 whatever default another module has set."""
+    was = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(was)
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def _qkv(seed, B, Sq, Sk, Hq, Hkv, D, dtype):
+    require_cuda()
+    g = torch.Generator().manual_seed(seed)
+    q = (1.5 * torch.randn(B, Sq, Hq, D, generator=g)).to(dtype)
+    k = torch.randn(B, Sk, Hkv, D, generator=g).to(dtype)
+    v = torch.randn(B, Sk, Hkv, D, generator=g).to(dtype)
+    return q.cuda(), k.cuda(), v.cuda()
+
+
+def _i32(*v):
+    return torch.tensor(v, dtype=torch.int32).cuda()
+
+
+def _run(seed, shape, dtype, **options):
+    q, k, v = _qkv(seed, *shape, dtype)
+    out = kb.attention_scored(q, k, v, **options)
+    torch.cuda.synchronize()
+    check_attention(out, q, k, v, what=(shape, dtype, sorted(options)), **options)
+    return q, k, v, out
+
+
+SHAPES = [
+    # B, Sq, Sk, Hq, Hkv, D
+    (1, 1, 1, 1, 1, 128), (2, 1, 130, 4, 2, 64), (1, 3, 127, 7, 1, 128), (2, 31, 31, 8, 8, 128), (1, 128, 128, 2, 2, 64),
+    (1, 129, 129, 1, 1, 128), (1, 151, 151, 2, 1, 128), (1, 257, 300, 3, 1, 64), (1, 65, 513, 4, 2, 128), (3, 2, 700, 8, 2, 128),
+    (1, 300, 300, 2, 2, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_full(shape, dtype):
+    _run(sum(shape), shape, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_all_options(shape, dtype):
+    """Cap, distance bias, causal with a prefix, ragged lengths and a start, together."""
+    B, Sq, Sk, Hq = shape[:4]
+    lengths = _i32(*[max(1, Sk - 13 * b) for b in range(B)])
+    _run(sum(shape) + 1, shape, dtype, cap=5.0, slopes=torch.exp2(-torch.arange(1, Hq + 1.0)).cuda(), causal=True,
+         prefix=_i32(*[Sk // 3 + b for b in range(B)]), kv_lengths=lengths, q_start=lengths - Sq, scale=0.11)
+
+
+@pytest.mark.parametrize("option", [dict(cap=50.0), dict(cap=0.7), dict(causal=True),
+                                    dict(slopes=torch.tensor([0.0, 0.5, 2.0, 0.01], dtype=torch.float32)), dict(scale=0.0), dict(scale=-0.3)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("Sq,Sk", [(200, 200), (5, 400)])
+def test_one_option(Sq, Sk, dtype, option):
+    option = {n: v.cuda() if torch.is_tensor(v) else v for n, v in option.items()}
+    _run(Sq + Sk, (2, Sq, Sk, 4, 2, 128), dtype, **option)
+
+
+def _documents(B, S, sizes):
+    d = torch.cat([torch.full((n,), i) for i, n in enumerate(sizes)])
+    d = torch.cat([d, torch.full((max(0, S - len(d)),), -1)])[:S]
+    return d.to(torch.int32).repeat(B, 1).cuda()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("sizes", [(400,), (1,) * 50, (60, 200, 7, 133), (128, 128, 128), (5, 0, 300, 40)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_documents(sizes, causal, dtype):
+    """Packed documents; tokens past the last one are in none (their queries see nothing)."""
+    S = 400
+    d = _documents(2, S, sizes)
+    _, _, _, out = _run(len(sizes), (2, S, S, 2, 1, 64), dtype, q_documents=d, kv_documents=d, causal=causal)
+    assert (out[d < 0] == 0).all()
+
+
+def test_documents_in_any_order():
+    g = torch.Generator().manual_seed(4)
+    d = torch.randint(-1, 5, (2, 333), generator=g, dtype=torch.int32).cuda()
+    _run(8, (2, 333, 333, 2, 2, 128), BF16, q_documents=d, kv_documents=d,
+         slopes=torch.tensor([0.1, 0.2]).cuda())
+    qd = d[:, :3].contiguous()
+    _run(9, (2, 3, 333, 4, 2, 128), BF16, q_documents=qd, kv_documents=d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("Sq,Sk", [(40, 300), (1, 300), (300, 300)])
+def test_rows_that_see_nothing(Sq, Sk, dtype):
+    """Lengths of zero, and causal queries before the first key."""
+    q, k, v, out = _run(1, (3, Sq, Sk, 2, 1, 64), dtype, kv_lengths=_i32(0, 1, Sk + 5))
+    assert (out[0] == 0).all()
+    _, _, _, out = _run(2, (2, Sq, Sk, 2, 1, 64), dtype, causal=True, q_start=_i32(-Sq - 3, -1))
+    assert (out[0] == 0).all() and (out[1, 0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_no_keys(dtype):
+    q, k, v = _qkv(1, 2, 5, 0, 4, 2, 64, dtype)
+    assert (kb.attention_scored(q, k, v) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("Sq,Sk", [(150, 150), (1, 150), (1, 1100), (300, 300)])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), float("-inf")])
+def test_unseen_keys_do_not_leak(Sq, Sk, dtype, poison):
+    """NaN and infinities in keys and values behind a length, ahead of a causal query, and in other
+    documents change nothing: every output is the definition's over the seen keys."""
+    q, k, v = _qkv(7, 2, Sq, Sk, 4, 2, 128, dtype)
+    n = Sk - 17
+    opts = dict(kv_lengths=_i32(n, Sk - 1))
+    k[0, n:], v[0, n:], k[1, Sk - 1:], v[1, Sk - 1:] = poison, poison, poison, poison
+    check_attention(kb.attention_scored(q, k, v, **opts), q, k, v, **opts)
+    at = Sk - min(Sq, 9)          # causal: queries before position `at` do not see it
+    q, k, v = _qkv(8, 1, Sq, Sk, 4, 2, 128, dtype)
+    k[0, at], v[0, at] = poison, poison
+    out = kb.attention_scored(q, k, v, causal=True)
+    first = at - (Sk - Sq)        # first query that sees it
+    if first > 0:
+        check_attention(out[:, :first], q[:, :first], k, v, causal=True, q_start=_i32(Sk - Sq))
+    d = torch.zeros(1, Sk, dtype=torch.int32)
+    d[0, Sk // 2:] = 1
+    d = d.cuda()
+    q, k, v = _qkv(9, 1, Sq, Sk, 4, 2, 128, dtype)
+    k[0, 3], v[0, 5] = poison, poison
+    qd = torch.ones(1, Sq, dtype=torch.int32).cuda()
+    check_attention(kb.attention_scored(q, k, v, q_documents=qd, kv_documents=d), q, k, v, q_documents=qd, kv_documents=d)
+
+
+def test_seen_nonfinite_values_are_seen():
+    q, k, v = _qkv(3, 1, 140, 140, 2, 2, 64, BF16)
+    v[0, 50, 0, 3] = float("nan")
+    out = kb.attention_scored(q, k, v, causal=True)
+    assert torch.isfinite(out[0, :50]).all() and torch.isnan(out[0, 50:, 0, 3]).all()
+    assert torch.isfinite(out[0, :, 1]).all() and torch.isfinite(out[0, :, 0, :3]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_strides(dtype):
+    """Views into a fused projection, heads before tokens, and an output inside a larger buffer."""
+    require_cuda()
+    g = torch.Generator().manual_seed(2)
+    qkv = torch.randn(2, 70, 3 * 4 * 64, generator=g).to(dtype).cuda()
+    q, k, v = (x.unflatten(2, (4, 64)) for x in qkv.split(256, 2))
+    check_attention(kb.attention_scored(q, k, v, causal=True), q, k, v, causal=True)
+    qh, kh, vh = (x.transpose(1, 2).contiguous().transpose(1, 2) for x in (q, k, v))
+    buf = torch.full((2, 80, 6, 64), 3.0, dtype=dtype, device="cuda")
+    out = kb.attention_scored(qh, kh, vh, out=buf[:, 5:75, 1:5])
+    check_attention(out, q, k, v)
+    buf[:, 5:75, 1:5] = 3.0
+    assert (buf == 3.0).all()
+
+
+def test_scores_that_grow_along_the_keys():
+    """The running maximum moves far in every tile, so every tile rescales what came before."""
+    q, k, v = _qkv(5, 1, 200, 900, 2, 1, 128, BF16)
+    k = (k.float() * torch.linspace(0.1, 6, 900, device="cuda")[None, :, None, None]).to(BF16)
+    check_attention(kb.attention_scored(q, k, v), q, k, v)
+    check_attention(kb.attention_scored(q[:, :2].contiguous(), k, v), q[:, :2], k, v)
+    big = (q.float() * 30).to(BF16)
+    check_attention(kb.attention_scored(big, k, v), big, k, v)
+
+
+def test_same_bits_again_and_on_another_stream():
+    q, k, v = _qkv(6, 3, 2, 1500, 8, 2, 128, BF16)
+    L = _i32(1500, 700, 3)
+    want = kb.attention_scored(q, k, v, kv_lengths=L, cap=30.0)
+    assert torch.equal(want, kb.attention_scored(q, k, v, kv_lengths=L, cap=30.0))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = kb.attention_scored(q, k, v, kv_lengths=L, cap=30.0)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(want, other)
+
+
+def test_two_captured_graphs():
+    """Two captured calls, each with its own workspace, replayed at the same time on two streams."""
+    sets = [_qkv(s, 2, 1, 3001, 8, 2, 128, BF16) for s in (1, 2)]
+    want = [kb.attention_scored(*s) for s in sets]
+    graphs, outs = [], []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(kb.attention_scored(*s))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert torch.equal(w, o)
+    kb.kernel_status()

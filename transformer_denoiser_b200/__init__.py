@@ -48,6 +48,12 @@ SIGNATURES = [
     ("kimodo_attention_f32", _I, [_P, _P, _P, _I, _I, _P]),
     ("kimodo_layernorm", _I, [_P, _P, _I, _P, _P, _I, _P]),
     ("kimodo_global_to_local_root", _I, [_P, _P, _P, _I, _I, _P, _P]),
+    ("kimodo_quantize_int8", _I, [_P, _LL, _I, _P, _LL, _P, _I, _I, _P]),
+    ("kimodo_rms_norm_int8", _I, [_P, _LL, _I, _P, _LL, _P, _LL, _I, _P, _F, _P, _LL, _P, _I, _I, _P]),
+    ("kimodo_gemm_int8", _I, [_P, _LL, _P, _P, _LL, _P, _P, _P, _LL, _P, _LL, _I, _I, _I, _I, _I, _P]),
+    ("kimodo_attention_scored_workspace", _I, [_P, _P]),
+    ("kimodo_attention_scored", _I, [_P, _P, _SZ, _P]),
+    ("kimodo_kernel_status", _I, [_P]),
 ]
 EPI_BIAS, EPI_BIAS_GELU, EPI_BIAS_SILU, EPI_BIAS_RESID = 0, 1, 2, 3
 
@@ -59,6 +65,16 @@ class SamplerOptions(ctypes.Structure):
     """struct kimodo_sampler of include/kimodo.h."""
     _fields_ = [("schedule", ctypes.c_int), ("eta", ctypes.c_float), ("step_noise", ctypes.c_void_p),
                 ("text_batch", ctypes.c_int)]
+
+
+class ScoredAttention(ctypes.Structure):
+    """struct kimodo_scored_attention of include/kimodo_kernels.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "out", "slopes", "prefix", "q_documents", "kv_documents",
+                                                "kv_lengths", "q_start")]
+                + [(n, ctypes.c_longlong * 3) for n in ("q_strides", "k_strides", "v_strides", "out_strides")]
+                + [(n, ctypes.c_int) for n in ("batch", "q_len", "kv_len", "q_heads", "kv_heads", "head_dim", "dtype",
+                                               "causal")]
+                + [("scale", ctypes.c_float), ("cap", ctypes.c_float)])
 
 
 class KimodoError(RuntimeError):
@@ -211,6 +227,197 @@ def global_to_local_root(root, x, lengths):
     out = torch.empty((B, T, MOTION_DIM), dtype=torch.float32, device=x.device)
     _check(lib.kimodo_global_to_local_root(_ptr(root), _ptr(x), _ptr(lengths), B, T, _ptr(out), _cur_stream()))
     return out
+
+
+# ------------------------------------------------------------ 8-bit projections, scored attention
+#
+# These take CUDA tensors of one device, which need not be the current one; work is enqueued
+# on that device's current stream and outputs are allocated there.
+
+def _same_device(*tensors):
+    """The CUDA device that all given tensors are on."""
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors are on different devices ({dev} and {t.device})")
+    return dev
+
+
+def _dtype_flag(t, what):
+    """1 for bf16, 0 for fp32."""
+    import torch
+    if t.dtype == torch.bfloat16:
+        return 1
+    if t.dtype == torch.float32:
+        return 0
+    raise ValueError(f"{what} must be bf16 or fp32 (got {t.dtype})")
+
+
+def _need(t, what, dtype, shape=None):
+    """Checks an optional contiguous tensor and returns its data pointer."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} (got {t.dtype}, {tuple(t.shape)})")
+    return t.data_ptr()
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, stream) on `dev`'s current stream, with `dev` current."""
+    import torch
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _rows_of(x, what):
+    """Row stride of a 2-D tensor with consecutive columns."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{what} must be a 2-D tensor with unit column stride")
+    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+
+
+def _int8_rows(rows, cols, dev):
+    """An int8 [rows, cols] tensor whose rows start on 16-byte boundaries, as gemm_int8 asks."""
+    import torch
+    if cols % 16 == 0:
+        return torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=dev)[:, :cols]
+
+
+def quantize_int8(x):
+    """(q, scale) of the rows of x [rows, cols] (fp32 or bf16): int8 [rows, cols] with rows on
+    16-byte boundaries and fp32 [rows], x ~ q * scale[:, None]."""
+    import torch
+    lib = load_library()
+    dev = _same_device(x)
+    flag, ldx = _dtype_flag(x, "x"), _rows_of(x, "x")
+    rows, cols = x.shape
+    q = _int8_rows(rows, cols, dev)
+    scale = torch.empty(rows, dtype=torch.float32, device=dev)
+    _launch(dev, lib.kimodo_quantize_int8, x.data_ptr(), ldx, flag, q.data_ptr(), q.stride(0), scale.data_ptr(), rows,
+            cols)
+    return q, scale
+
+
+def rms_norm_int8(x, gamma, residual=None, eps=1e-6, residual_out=None):
+    """(q, scale, residual_out): int8 rows and fp32 scales of the RMS norm of x + residual times
+    gamma (fp32 [cols]), and the sum in the residual's type (None without a residual).
+    x and residual [rows, cols], fp32 or bf16; residual_out may be residual itself."""
+    import torch
+    lib = load_library()
+    dev = _same_device(x, gamma, residual, residual_out)
+    flag, ldx = _dtype_flag(x, "x"), _rows_of(x, "x")
+    rows, cols = x.shape
+    rp = rop = None
+    ldr = ldro = rflag = 0
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError("residual must have the shape of x")
+        if residual_out is None:
+            residual_out = torch.empty((rows, cols), dtype=residual.dtype, device=dev)
+        elif residual_out.shape != x.shape or residual_out.dtype != residual.dtype:
+            raise ValueError("residual_out must have the shape and type of residual")
+        rflag, ldr, ldro = _dtype_flag(residual, "residual"), _rows_of(residual, "residual"), _rows_of(residual_out, "residual_out")
+        rp, rop = residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    q = _int8_rows(rows, cols, dev)
+    scale = torch.empty(rows, dtype=torch.float32, device=dev)
+    _launch(dev, lib.kimodo_rms_norm_int8, x.data_ptr(), ldx, flag, rp, ldr, rop, ldro, rflag,
+            _need(gamma, "gamma", torch.float32, (cols,)), float(eps), q.data_ptr(), q.stride(0), scale.data_ptr(), rows,
+            cols)
+    return q, scale, residual_out
+
+
+def gemm_int8(a, a_scale, w, w_scale, bias=None, epilogue=EPI_BIAS, out_f32=False, resid=None, out=None):
+    """out = epilogue(a_scale[:, None] * w_scale * (a w^T) + bias): int8 a [M, K], w [N, K] (rows on
+    16-byte boundaries), fp32 scales [M], [N] and bias [N] or None; out bf16 or fp32 [M, N];
+    resid fp32 [M, N] with EPI_BIAS_RESID (may be out)."""
+    import torch
+    lib = load_library()
+    dev = _same_device(a, a_scale, w, w_scale, bias, resid, out)
+    if a.dtype != torch.int8 or w.dtype != torch.int8:
+        raise ValueError("a and w must be int8")
+    lda, ldw = _rows_of(a, "a"), _rows_of(w, "w")
+    (M, K), N = a.shape, w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"a has {K} columns, w {w.shape[1]}")
+    if M == 1:   # the stride of a single row is never used
+        lda = (K + 15) // 16 * 16
+    if N == 1:
+        ldw = (K + 15) // 16 * 16
+    dtype = torch.float32 if out_f32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=dev)
+    elif out.dtype != dtype or tuple(out.shape) != (M, N):
+        raise ValueError(f"out must be a {dtype} tensor of shape {(M, N)}")
+    if resid is not None and (resid.dtype != torch.float32 or tuple(resid.shape) != (M, N)):
+        raise ValueError(f"resid must be an fp32 tensor of shape {(M, N)}")
+    _launch(dev, lib.kimodo_gemm_int8, a.data_ptr(), lda, _need(a_scale, "a_scale", torch.float32, (M,)), w.data_ptr(),
+            ldw, _need(w_scale, "w_scale", torch.float32, (N,)), _need(bias, "bias", torch.float32, (N,)),
+            None if resid is None else resid.data_ptr(), 0 if resid is None else _rows_of(resid, "resid"),
+            out.data_ptr(), _rows_of(out, "out"), M, N, K, int(epilogue), int(bool(out_f32)))
+    return out
+
+
+def attention_scored(q, k, v, scale=None, cap=0.0, slopes=None, causal=False, prefix=None, q_documents=None,
+                     kv_documents=None, kv_lengths=None, q_start=None, out=None):
+    """Attention of q [B, Sq, Hq, D] over k, v [B, Sk, Hkv, D] (bf16 or fp32, D 64 or 128, last
+    dimension consecutive, other strides free in multiples of 16 bytes); head h reads key
+    head h // (Hq // Hkv).  scale: default D ** -0.5; cap > 0: cap * tanh(score / cap); slopes
+    fp32 [Hq]: minus slope * |position distance|; causal, with prefix int32 [B] keys seen by
+    all; documents int32 [B, Sq], [B, Sk]: only equal numbers >= 0 meet; kv_lengths int32
+    [B]; q_start int32 [B]: position of the first query (default Sk - Sq).  A query that sees
+    no key gets 0.  Returns [B, Sq, Hq, D]."""
+    import torch
+    lib = load_library()
+    dev = _same_device(q, k, v, slopes, prefix, q_documents, kv_documents, kv_lengths, q_start, out)
+    bf = _dtype_flag(q, "q")
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be 4-D [batch, tokens, heads, dims]")
+    (B, Sq, Hq, D), (Bk, Sk, Hkv, Dk) = q.shape, k.shape
+    if k.dtype != q.dtype or v.dtype != q.dtype or v.shape != k.shape or Bk != B or Dk != D:
+        raise ValueError("q, k and v must agree in type, batch and dims, and k and v in shape")
+    if out is None:
+        out = torch.empty((B, Sq, Hq, D), dtype=q.dtype, device=dev)
+    elif out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must have the shape and type of q")
+    strides = []
+    for t, what in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+        s = t.stride()
+        if s[3] != 1:
+            raise ValueError(f"the last dimension of {what} must be consecutive")
+        strides.append(s[:3])
+    i32 = torch.int32
+    args = ScoredAttention(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _need(slopes, "slopes", torch.float32, (Hq,)),
+        _need(prefix, "prefix", i32, (B,)), _need(q_documents, "q_documents", i32, (B, Sq)),
+        _need(kv_documents, "kv_documents", i32, (B, Sk)), _need(kv_lengths, "kv_lengths", i32, (B,)),
+        _need(q_start, "q_start", i32, (B,)), *strides, B, Sq, Sk, Hq, Hkv, D, BF16 if bf else FP32, int(bool(causal)),
+        D ** -0.5 if scale is None else float(scale), float(cap))
+    ref = ctypes.byref(args)
+    if not bf:
+        _launch(dev, lib.kimodo_attention_scored, ref, None, 0)
+        return out
+    size = ctypes.c_size_t()
+    with torch.cuda.device(dev):
+        _check(lib.kimodo_attention_scored_workspace(ref, ctypes.byref(size)))
+        ws = torch.empty(size.value, dtype=torch.uint8, device=dev) if size.value else None
+        _launch(dev, lib.kimodo_attention_scored, ref, None if ws is None else ws.data_ptr(), size.value)
+    return out
+
+
+def kernel_status(device=None):
+    """Synchronise the current stream and raise if a wait in a kernel-level call ran out."""
+    import torch
+    lib = load_library()
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        _check(lib.kimodo_kernel_status(torch.cuda.current_stream().cuda_stream))
 
 
 class Kimodo:

@@ -18,7 +18,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkimodo.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-SOURCES = ["gemm_tc.cu", "gemm_tc2.cu", "gemm_f32.cu", "attention.cu", "attention_tc.cu", "layernorm.cu", "motion.cu", "capi.cu"]
+SOURCES = ["gemm_tc.cu", "gemm_tc2.cu", "gemm_f32.cu", "gemm_i8.cu", "attention.cu", "attention_tc.cu", "attention_scored.cu",
+           "layernorm.cu", "quant.cu", "motion.cu", "status.cu", "capi.cu", "capi_ops.cu"]
 
 
 def nvcc() -> str:
@@ -33,7 +34,7 @@ def _needs_rebuild(obj: str, src: str) -> bool:
         return True
     t = os.path.getmtime(obj)
     deps = [src] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    deps.append(os.path.join(ROOT, "include", "kimodo.h"))
+    deps += [os.path.join(ROOT, "include", h) for h in ("kimodo.h", "kimodo_kernels.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -11,7 +11,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
-#include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
@@ -28,36 +27,11 @@
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "status.h"
 
 using namespace kd;
 
 namespace {
-
-thread_local std::string g_last_error;
-
-int set_error(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return code;
-}
-
-#define KD_CUDA(call)                                                                              \
-  do {                                                                                             \
-    cudaError_t e_ = (call);                                                                       \
-    if (e_ != cudaSuccess)                                                                         \
-      return set_error(e_ == cudaErrorMemoryAllocation ? KIMODO_ENOMEM : KIMODO_ECUDA, "%s: %s (%s:%d)", \
-                       #call, cudaGetErrorString(e_), __FILE__, __LINE__);                         \
-  } while (0)
-
-#define KD_TRY(call)        \
-  do {                      \
-    int s_ = (call);        \
-    if (s_ != KIMODO_OK) return s_; \
-  } while (0)
 
 #ifndef KD_SAMPLE_GROUPS
 #define KD_SAMPLE_GROUPS 2
@@ -546,8 +520,6 @@ int pack_root_input(kimodo_ctx* c, int B, int nseq, int T, cudaStream_t st) {
   });
 }
 
-bool is_device_memory(const void* p);
-
 // Chooses the token layout of a call (lengths already validated when on the host) and,
 // for the packed layout, enqueues the token map built from the staged lengths.
 Tokens plan_tokens(const int* lengths, int batch, int nseq, int frames) {
@@ -573,15 +545,6 @@ int enqueue_token_map(kimodo_ctx* c, int batch, int nseq, cudaStream_t st) {
 
 // ------------------------------------------------------------------ argument checks
 
-bool is_device_memory(const void* p) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  return a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged;
-}
-
 int check_ctx(kimodo_ctx* c) {
   if (!c) return set_error(KIMODO_EINVAL, "ctx is NULL");
   KD_CUDA(cudaSetDevice(c->device));
@@ -606,18 +569,6 @@ int stage_lengths(kimodo_ctx* c, const int* lengths, int batch, int frames, cuda
   }
   KD_CUDA(cudaMemcpyAsync(c->ws.lengths, lengths, (size_t)batch * 4, cudaMemcpyDefault, st));
   return KIMODO_OK;
-}
-
-const char* where_name(int where) {
-  switch (where) {
-    case WHERE_GEMM_PRODUCER: return "GEMM TMA producer";
-    case WHERE_GEMM_MMA: return "GEMM MMA issuer";
-    case WHERE_GEMM_EPILOGUE: return "GEMM epilogue";
-    case WHERE_GEMM_DRAIN: return "GEMM MMA drain";
-    case WHERE_ATTENTION: return "attention";
-    case WHERE_WAIT_SELFTEST: return "wait self-test";
-    default: return "unknown stage";
-  }
 }
 
 // One CTA, one thread: a bounded wait on an mbarrier that nothing arrives on, with the
@@ -653,10 +604,10 @@ int finish_outputs(kimodo_ctx* c, const void* out, cudaStream_t st) {
 
 extern "C" {
 
-const char* kimodo_last_error(void) { return g_last_error.c_str(); }
+const char* kimodo_last_error(void) { return last_error(); }
 
 int kimodo_load_weights(kimodo_ctx** out_ctx, const float* host_blob, size_t n_floats, int precision, int device) {
-  g_last_error.clear();
+  clear_error();
   if (!out_ctx) return set_error(KIMODO_EINVAL, "ctx out-pointer is NULL");
   *out_ctx = nullptr;
   if (!host_blob) return set_error(KIMODO_EINVAL, "weight blob is NULL");
@@ -776,7 +727,7 @@ void kimodo_free(kimodo_ctx* c) {
 
 int kimodo_denoiser_forward(kimodo_ctx* c, int net, const float* x, const float* emb, int t, const int* lengths,
                             int batch, int frames, float* out, void* stream) {
-  g_last_error.clear();
+  clear_error();
   KD_TRY(check_ctx(c));
   if (net != KIMODO_NET_ROOT && net != KIMODO_NET_BODY) return set_error(KIMODO_EINVAL, "net must be 0 or 1");
   if (!x || !emb || !out) return set_error(KIMODO_EINVAL, "NULL tensor argument");
@@ -859,7 +810,7 @@ int kimodo_ddim_step(kimodo_ctx* c, const float* x_t, const float* text_emb, con
 int kimodo_ddim_step_ex(kimodo_ctx* c, const float* x_t, const float* text_emb, const float* null_emb,
                         int null_batch, const int* lengths, int batch, int frames, int t, int t_prev,
                         float cfg_scale, const kimodo_sampler* options, float* x_prev, void* stream) {
-  g_last_error.clear();
+  clear_error();
   KD_TRY(check_ctx(c));
   if (!x_t || !text_emb || !null_emb || !x_prev) return set_error(KIMODO_EINVAL, "NULL tensor argument");
   KD_TRY(check_shape(batch, frames));
@@ -985,7 +936,7 @@ int kimodo_ddim_sample(kimodo_ctx* c, const float* text_emb, const float* null_e
 int kimodo_ddim_sample_ex(kimodo_ctx* c, const float* text_emb, const float* null_emb, int null_batch,
                           const float* noise, const int* lengths, int batch, int frames, int steps, float cfg_scale,
                           const kimodo_sampler* options, float* out, void* stream) {
-  g_last_error.clear();
+  clear_error();
   KD_TRY(check_ctx(c));
   if (!text_emb || !null_emb || !noise || !out) return set_error(KIMODO_EINVAL, "NULL tensor argument");
   KD_TRY(check_shape(batch, frames));
@@ -1063,7 +1014,7 @@ int kimodo_ddim_sample_ex(kimodo_ctx* c, const float* text_emb, const float* nul
 }
 
 int kimodo_sync_status(kimodo_ctx* c, void* stream) {
-  g_last_error.clear();
+  clear_error();
   KD_TRY(check_ctx(c));
   KD_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
   DevError h;
@@ -1076,7 +1027,7 @@ int kimodo_sync_status(kimodo_ctx* c, void* stream) {
 }
 
 int kimodo_wait_selftest(kimodo_ctx* c, int limit_us, void* stream) {
-  g_last_error.clear();
+  clear_error();
   KD_TRY(check_ctx(c));
   if (limit_us < 1 || limit_us > 2000000) return set_error(KIMODO_EINVAL, "limit_us must be in [1, 2000000]");
   wait_selftest_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(c->derr, 1000ull * (unsigned)limit_us);
@@ -1085,7 +1036,7 @@ int kimodo_wait_selftest(kimodo_ctx* c, int limit_us, void* stream) {
 }
 
 int kimodo_profile_enable(kimodo_ctx* c, int enable) {
-  g_last_error.clear();
+  clear_error();
   if (!c) return set_error(KIMODO_EINVAL, "ctx is NULL");
   c->profiling = enable != 0;
   c->prof.clear();
@@ -1095,7 +1046,7 @@ int kimodo_profile_enable(kimodo_ctx* c, int enable) {
 
 int kimodo_profile_read(kimodo_ctx* c, int n_classes, double* ms, long long* launches, double* flops,
                         double* bytes) {
-  g_last_error.clear();
+  clear_error();
   KD_TRY(check_ctx(c));
   if (n_classes < 1 || n_classes > NUM_CLS) return set_error(KIMODO_EINVAL, "n_classes must be in [1, 8]");
   for (int i = 0; i < n_classes; ++i) {
@@ -1127,14 +1078,6 @@ long long kimodo_last_launch_count(kimodo_ctx* c) { return c ? c->last_launches 
 
 namespace {
 
-DevError* kernel_error_word() {
-  static DevError* p[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-  if (!p[dev] && cudaMalloc(&p[dev], sizeof(DevError)) == cudaSuccess) cudaMemset(p[dev], 0, sizeof(DevError));
-  return p[dev];
-}
-
 int prepared_device() {
   static bool done[64] = {};
   int dev = 0;
@@ -1165,7 +1108,7 @@ extern "C" {
 
 int kimodo_gemm_bf16(const void* A, int lda, const void* W, int ldw, const float* bias, const void* resid, int ldr,
                      void* out, int ldo, int M, int N, int K, int epilogue, int out_f32, int tile_n, void* stream) {
-  g_last_error.clear();
+  clear_error();
   KD_TRY(check_gemm_args(A, lda, W, ldw, bias, resid, out, ldo, M, N, K, epilogue));
   if (lda % 8 || ldw % 8 || (reinterpret_cast<uintptr_t>(A) & 15) || (reinterpret_cast<uintptr_t>(W) & 15))
     return set_error(KIMODO_EINVAL, "bf16 operands need 16-byte aligned rows (lda, ldw multiples of 8)");
@@ -1196,7 +1139,7 @@ int kimodo_gemm_bf16(const void* A, int lda, const void* W, int ldw, const float
 int kimodo_gemm_bf16_pair(const void* A, int lda, const void* W, int ldw, const float* bias, const void* resid,
                           int ldr, void* out, int ldo, int M, int N, int K, int epilogue, int out_f32, int tile_n,
                           void* stream) {
-  g_last_error.clear();
+  clear_error();
   KD_TRY(check_gemm_args(A, lda, W, ldw, bias, resid, out, ldo, M, N, K, epilogue));
   if (lda % 8 || ldw % 8 || (reinterpret_cast<uintptr_t>(A) & 15) || (reinterpret_cast<uintptr_t>(W) & 15))
     return set_error(KIMODO_EINVAL, "bf16 operands need 16-byte aligned rows (lda, ldw multiples of 8)");
@@ -1223,7 +1166,7 @@ int kimodo_gemm_bf16_pair(const void* A, int lda, const void* W, int ldw, const 
 
 int kimodo_gemm_f32(const float* A, int lda, const float* W, int ldw, const float* bias, const float* resid, int ldr,
                     float* out, int ldo, int M, int N, int K, int epilogue, void* stream) {
-  g_last_error.clear();
+  clear_error();
   KD_TRY(check_gemm_args(A, lda, W, ldw, bias, resid, out, ldo, M, N, K, epilogue));
   if (K % 16 || lda % 4 || ldw % 4) return set_error(KIMODO_EINVAL, "fp32 GEMM needs K % 16 == 0, lda/ldw % 4 == 0");
   GemmArgs g;
@@ -1235,7 +1178,7 @@ int kimodo_gemm_f32(const float* A, int lda, const float* W, int ldw, const floa
 }
 
 int kimodo_attention_bf16(const void* qkv, void* out, const int* lengths, int nseq, int S, void* stream) {
-  g_last_error.clear();
+  clear_error();
   if (!qkv || !out || !lengths) return set_error(KIMODO_EINVAL, "NULL tensor argument");
   if (nseq < 1 || S < 1 || S > MAX_FRAMES + 1) return set_error(KIMODO_EINVAL, "need nseq >= 1, 1 <= S <= 301");
   if (reinterpret_cast<uintptr_t>(qkv) & 15) return set_error(KIMODO_EINVAL, "qkv must be 16-byte aligned");
@@ -1246,7 +1189,7 @@ int kimodo_attention_bf16(const void* qkv, void* out, const int* lengths, int ns
 }
 
 int kimodo_attention_f32(const float* qkv, float* out, const int* lengths, int nseq, int S, void* stream) {
-  g_last_error.clear();
+  clear_error();
   if (!qkv || !out || !lengths) return set_error(KIMODO_EINVAL, "NULL tensor argument");
   if (nseq < 1 || S < 1 || S > MAX_FRAMES + 1) return set_error(KIMODO_EINVAL, "need nseq >= 1, 1 <= S <= 301");
   KD_CUDA(attention_f32(qkv, out, lengths, nseq, nseq, S, static_cast<cudaStream_t>(stream)));
@@ -1255,7 +1198,7 @@ int kimodo_attention_f32(const float* qkv, float* out, const int* lengths, int n
 
 int kimodo_layernorm(const float* y, void* out, int out_bf16, const float* gamma, const float* beta, int M,
                      void* stream) {
-  g_last_error.clear();
+  clear_error();
   if (!y || !out || !gamma || !beta) return set_error(KIMODO_EINVAL, "NULL tensor argument");
   if (M < 1) return set_error(KIMODO_EINVAL, "M must be >= 1");
   KD_CUDA(layernorm(y, out, out_bf16 != 0, gamma, beta, M, static_cast<cudaStream_t>(stream)));
@@ -1264,7 +1207,7 @@ int kimodo_layernorm(const float* y, void* out, int out_bf16, const float* gamma
 
 int kimodo_global_to_local_root(const float* root, const float* x, const int* lengths, int batch, int frames,
                                 float* body_in, void* stream) {
-  g_last_error.clear();
+  clear_error();
   if (!root || !x || !lengths || !body_in) return set_error(KIMODO_EINVAL, "NULL tensor argument");
   KD_TRY(check_shape(batch, frames));
   // The kernel places frame i of sequence s at row s * S + 1 + i of its output matrix
@@ -1389,7 +1332,7 @@ struct WorkspaceSwap {
 extern "C" int kimodo_denoiser_forward_noalloc(kimodo_ctx* c, int net, const float* x, const float* emb, int t,
                                                const int* lengths, int batch, int frames, float* out,
                                                void* stream) {
-  g_last_error.clear();
+  clear_error();
   KD_TRY(check_ctx(c));
   if (net != KIMODO_NET_ROOT && net != KIMODO_NET_BODY) return set_error(KIMODO_EINVAL, "net must be 0 or 1");
   if (!x || !emb || !out) return set_error(KIMODO_EINVAL, "NULL tensor argument");

@@ -51,6 +51,7 @@ enum DevErrWhere : int {
   WHERE_GEMM_DRAIN = 4,
   WHERE_ATTENTION = 5,
   WHERE_WAIT_SELFTEST = 6,
+  WHERE_SCORED_ATTENTION = 7,
 };
 
 }  // namespace kd

@@ -369,6 +369,42 @@ int make_tmap_plain(CUtensorMap* m, const void* base, int elem, int rows, int co
   return r == CUDA_SUCCESS ? 0 : -3;
 }
 
+// Row-major 8-bit matrix [rows, ld] whose first `cols` columns are the K extent: boxes of
+// 128 columns x box_rows rows, 128-byte swizzle, zero fill.
+int make_tmap_i8(CUtensorMap* m, const void* base, int rows, int cols, long ld, int box_rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return -1;
+  if ((reinterpret_cast<uintptr_t>(base) & 15) || ld % 16) return -2;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -3;
+}
+
+// Keys or values bf16 [batch][token][head][dims] with any strides (elements, multiples of 8;
+// the dims consecutive): boxes of 64 dims x 128 tokens, 128-byte swizzle, zero fill.  The
+// coordinates are (dim, token, head, sequence).
+int make_tmap_heads(CUtensorMap* m, const void* base, int dims_, int tokens, int heads, int batch, long s_token,
+                    long s_head, long s_batch) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return -1;
+  if (reinterpret_cast<uintptr_t>(base) & 15) return -2;
+  cuuint64_t dims[4] = {(cuuint64_t)dims_, (cuuint64_t)tokens, (cuuint64_t)heads, (cuuint64_t)batch};
+  // the stride of an extent of one is never used; any valid value does
+  cuuint64_t strides[3] = {(cuuint64_t)(tokens > 1 ? s_token : dims_) * 2, (cuuint64_t)(heads > 1 ? s_head : dims_) * 2,
+                           (cuuint64_t)(batch > 1 ? s_batch : dims_) * 2};
+  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -3;
+}
+
 // Dispatch on (tile N, epilogue kind, output type).  The residual is fp32 (the
 // residual stream of the post-norm layers is kept in fp32; operands are bf16).
 static cudaError_t dispatch(const GemmArgs& g, int bn, int kind, bool out_f32, const EpiParams& ep, DevError* err,

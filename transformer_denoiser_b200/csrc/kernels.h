@@ -108,4 +108,80 @@ cudaError_t pack_embeddings(const float* text_emb, int B, const float* null_emb,
 cudaError_t gather_timestep_rows(const float* pe, int t_single, int steps, int n, void* out, bool out_bf16,
                                  cudaStream_t st);
 
+// ---- 8-bit projections and attention with scored masks (kernel-level entry points)
+
+// Rows in 8-bit integers: q = rint(127 t / max |t|), scale = max |t| / 127, with t = x or
+// (rms_norm_rows_int8) t = h gamma / sqrt(mean h^2 + eps), h = x + r_in (null: h = x), whose
+// fp32 sum is stored in r_out (may equal r_in) rounded to the residual's type.  x and the
+// residual are fp32 or bf16; leading dimensions in elements; 1 <= cols <= 32768.
+struct RowsInt8 {
+  const void* x = nullptr;
+  long ldx = 0;
+  const void* r_in = nullptr;
+  long ldr_in = 0;
+  void* r_out = nullptr;
+  long ldr_out = 0;
+  const float* gamma = nullptr;
+  int8_t* q = nullptr;
+  long ldq = 0;
+  float* scale = nullptr;
+  int rows = 0, cols = 0;
+  float eps = 0.f;
+};
+constexpr int ROWS_INT8_MAX_COLS = 32768;
+cudaError_t quantize_rows_int8(const RowsInt8& a, bool x_bf16, cudaStream_t st);
+cudaError_t rms_norm_rows_int8(const RowsInt8& a, bool x_bf16, bool r_bf16, cudaStream_t st);
+
+// out[m, n] = epilogue(a_scale[m] w_scale[n] sum_k A[m, k] W[n, k] + bias[n]); A, W int8 with
+// 16-byte aligned rows, bias may be null; kind and output type as the bf16 GEMM.
+struct GemmI8 {
+  const void* A = nullptr;
+  const void* W = nullptr;
+  const float* a_scale = nullptr;
+  const float* w_scale = nullptr;
+  const float* bias = nullptr;
+  const float* resid = nullptr;
+  void* out = nullptr;
+  int M = 0, N = 0, K = 0;
+  long lda = 0, ldw = 0, ldr = 0, ldo = 0;
+};
+cudaError_t gemm_i8(const GemmI8& g, int kind, bool out_f32, DevError* err, cudaStream_t st, int num_sms);
+int make_tmap_i8(CUtensorMap* m, const void* base, int rows, int cols, long ld, int box_rows);
+int make_tmap_heads(CUtensorMap* m, const void* base, int dims, int tokens, int heads, int batch, long s_token,
+                    long s_head, long s_batch);
+
+// Attention with scored masks (definition in attention_scored.cu).  q, out [B][Sq][Hq][HD],
+// k, v [B][Sk][Hkv][HD] by strides in elements, dims consecutive; HD 64 or 128; null optional
+// pointers switch their option off.
+struct ScoredAttention {
+  const void* q = nullptr;
+  const void* k = nullptr;
+  const void* v = nullptr;
+  void* out = nullptr;
+  const float* slopes = nullptr;     // [Hq]
+  const int* prefix = nullptr;       // [B], with causal
+  const int* q_doc = nullptr;        // [B][Sq], with kv_doc
+  const int* kv_doc = nullptr;       // [B][Sk]
+  const int* kv_lengths = nullptr;   // [B]
+  const int* q_start = nullptr;      // [B]; null: Sk - Sq
+  long q_batch = 0, q_token = 0, q_head = 0, k_batch = 0, k_token = 0, k_head = 0;
+  long v_batch = 0, v_token = 0, v_head = 0, o_batch = 0, o_token = 0, o_head = 0;
+  int B = 0, Sq = 0, Sk = 0, Hq = 0, Hkv = 0, G = 0, HD = 0;
+  float scale = 0.f, cap = 0.f;
+  int causal = 0;
+};
+// Split of a call over CTAs and keys; parts > 1: results of each part and their weights in a
+// workspace of `bytes`, joined by a second kernel.
+struct ScoredPlan {
+  int splits = 1, tiles_per_split = 1, row_blocks = 1, parts = 1;
+  bool alternate = false;
+  float* part_o = nullptr;
+  float* part_lse = nullptr;
+  size_t bytes = 0;
+};
+ScoredPlan scored_attention_plan(const ScoredAttention& a, int num_sms);
+cudaError_t attention_scored_bf16(const ScoredAttention& a, ScoredPlan plan, void* workspace, DevError* err,
+                                  cudaStream_t st);
+cudaError_t attention_scored_f32(const ScoredAttention& a, cudaStream_t st);
+
 }  // namespace kd
