@@ -401,9 +401,6 @@ def attention_scored(q, k, v, scale=None, cap=0.0, slopes=None, causal=False, pr
         _need(q_start, "q_start", i32, (B,)), *strides, B, Sq, Sk, Hq, Hkv, D, BF16 if bf else FP32, int(bool(causal)),
         D ** -0.5 if scale is None else float(scale), float(cap))
     ref = ctypes.byref(args)
-    if not bf:
-        _launch(dev, lib.kimodo_attention_scored, ref, None, 0)
-        return out
     size = ctypes.c_size_t()
     with torch.cuda.device(dev):
         _check(lib.kimodo_attention_scored_workspace(ref, ctypes.byref(size)))

@@ -9,17 +9,22 @@
 //
 // Rows of a tile.  The Sq queries of the G query heads that share a key head are one list of
 // Sq * G rows (token-major), so grouped heads share every key tile they load and a few new
-// tokens fill one MMA tile together.  A CTA takes 256 rows as two 128-row tiles: while the
-// softmax of one runs, the tensor cores work on the other.  With at most 128 rows (new
-// tokens over a cache) both halves take the same rows and alternate over the key tiles;
-// keys are also split over CTAs, and a second kernel joins the parts.
+// tokens fill one MMA tile together.
 //
-// Roles (384 threads): warp 0 TMA of K and V tiles (128 keys, 128-byte swizzle), warp 1 MMA
-// issue, warps 4-7 and 8-11 softmax and output of tile 0 and 1, one row a thread.  Per key
-// tile and row tile: S = Q K^T into 128 TMEM columns; the row's thread reads S, forms p and
-// writes it in bf16 over S; O += P V with P as the TMEM operand.  The running maximum is a
-// reference that moves only when it falls 2^8 behind (p stays below 2^8, which fp32 sums
-// and bf16 weights hold as well as 1), so O is rarely rescaled.
+// Many rows (scored_tc_kernel): a CTA takes 256 rows as two 128-row tiles; while the softmax
+// of one runs, the tensor cores work on the other.  Roles (384 threads): warp 0 TMA of K and
+// V tiles (128 keys, 128-byte swizzle), warp 1 MMA issue, warps 4-7 and 8-11 softmax and
+// output of tile 0 and 1, one row a thread.  Per key tile and row tile: S = Q K^T into 128
+// TMEM columns; the row's thread reads S, forms p and writes it in bf16 over S; O += P V with
+// P as the TMEM operand.
+//
+// Few rows (scored_few_kernel, at most 64: new tokens over a cache): the keys take the MMA's
+// rows instead, S^T = K Q^T and O^T = V^T P^T, so that all four TMEM quarters, and with them
+// all softmax warps, share a key tile however few the queries are, and an MMA costs N = rows.
+//
+// Keys are split over CTAs while these do not fill the SMs; a second kernel joins the parts.
+// The running maximum is a reference that moves only when it falls 2^8 behind (p stays below
+// 2^8, which fp32 sums and bf16 weights hold as well as 1), so O is rarely rescaled.
 //
 // Masked places never reach a result: a masked score is replaced, value rows past kv_len are
 // zeroed in shared memory, and a row whose result is not finite (a NaN or infinity among
@@ -52,10 +57,39 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// cap * tanh(x / cap) in log2 units: tanh z = 1 - 2 / (1 + e^(2z)), absolute error a few 2^-23
-__device__ __forceinline__ float capped(float s, float two_log2e_scale_over_cap, float cap_log2) {
-  const float e = ex2(s * two_log2e_scale_over_cap);
-  return fmaf(-2.f * cap_log2, rcp_approx(1.f + e), cap_log2);
+// cap * tanh(x / cap) in log2 units.  For |x| <= cap: x * R((x / cap)^2) with R(u) = tanh(sqrt u) /
+// sqrt u by a polynomial of degree 6 (weighted least squares towards the relative minimax on
+// [0, 1]; relative error 5.0e-8), which costs no special-function slots: those are what bounds
+// the softmax.  Beyond (rare: the tile is then done again), tanh z = 1 - 2 / (1 + e^(2z)).
+struct CapCoef {
+  float z, lin;          // scale / cap; scale * log2 e
+  float limit;           // |s| up to which the polynomial holds
+  float two, cap2;       // e^(2 s z) = 2^(two s); cap * log2 e
+};
+__device__ __forceinline__ CapCoef cap_coef(float scale, float cap) {
+  CapCoef k;
+  k.z = scale / cap;
+  k.lin = scale * LOG2E;
+  k.limit = 1.f / fabsf(k.z);
+  k.two = 2.f * LOG2E * k.z;
+  k.cap2 = cap * LOG2E;
+  return k;
+}
+// two scores at once (f32x2 arithmetic)
+__device__ __forceinline__ float2 capped_poly(const CapCoef& k, float2 s) {
+  const float2 z = __fmul2_rn(s, make_float2(k.z, k.z));
+  const float2 u = __fmul2_rn(z, z);
+  auto step = [&](float2 r, float c) { return __ffma2_rn(r, u, make_float2(c, c)); };
+  float2 r = step(make_float2(0.0010410185204818845f, 0.0010410185204818845f), -0.006203366909176111f);
+  r = step(r, 0.020289966836571693f);
+  r = step(r, -0.053457021713256836f);
+  r = step(r, 0.13325203955173492f);
+  r = step(r, -0.33332839608192444f);
+  r = step(r, 0.9999999403953552f);
+  return __fmul2_rn(__fmul2_rn(s, make_float2(k.lin, k.lin)), r);
+}
+__device__ __forceinline__ float capped_any(const CapCoef& k, float s) {
+  return fmaf(-2.f * k.cap2, rcp_approx(1.f + ex2(s * k.two)), k.cap2);
 }
 
 __device__ __forceinline__ void record_timeout(DevError* err, volatile int* abort) {
@@ -90,7 +124,7 @@ __device__ __forceinline__ int last_key(const ScoredAttention& a, const SeqInfo&
 
 // ---------------------------------------------------------------- one row by one warp, fp32
 // The definition, over the seen keys alone: scores by warp-shuffle dot products, online
-// softmax.  The fp32 path, and the rows of the bf16 path whose first result is not finite.
+// softmax.  For the rows whose first result is not finite.
 template <typename T, int HD>
 __device__ __noinline__ void row_by_warp(const ScoredAttention& a, int b, int hq, int i) {
   constexpr int PER = HD / 32;
@@ -137,18 +171,6 @@ __device__ __noinline__ void row_by_warp(const ScoredAttention& a, int b, int hq
   for (int e = 0; e < PER; ++e) out[e] = from_f<T>(l == 0.f ? 0.f : o[e] / l);
 }
 
-template <int HD>
-__global__ void __launch_bounds__(128) scored_f32_kernel(const __grid_constant__ ScoredAttention a) {
-  ptx::pdl_wait();
-  ptx::pdl_trigger();
-  const long rows = (long)a.B * a.Sq * a.Hq;
-  const long r = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (r >= rows) return;
-  const int hq = (int)(r % a.Hq);
-  const long bi = r / a.Hq;
-  row_by_warp<float, HD>(a, (int)(bi / a.Sq), hq, (int)(bi % a.Sq));
-}
-
 // ---------------------------------------------------------------- bf16: tcgen05
 
 template <int HD>
@@ -158,7 +180,7 @@ struct Cfg {
   static constexpr uint32_t HALF = TILE * 128;             // 64 dims of a tile
   // HD 64 would let two CTAs share an SM, whose TMEM holds one: the size keeps them apart
   static constexpr size_t BODY = 2 * Q_BYTES + (size_t)STAGES * KV_BYTES;
-  static constexpr size_t SMEM = 1024 + (BODY < 120000 ? 120000 / 1024 * 1024 : BODY) + MAX_FLAGS + 256;
+  static constexpr size_t SMEM = 1024 + (BODY < 119808 ? 119808 : BODY) + MAX_FLAGS + 256 + 8 * TILE * 4;
 };
 constexpr uint32_t TMEM_COLS = 512;
 __device__ __forceinline__ uint32_t s_col(int t) { return 128u * t; }
@@ -183,7 +205,7 @@ struct RowTile {
 };
 
 template <int HD, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(NUM_THREADS, 1)   // 168 registers a thread
 scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ ScoredAttention a, const ScoredPlan plan, DevError* err) {
   using C = Cfg<HD>;
@@ -203,6 +225,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 7);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   RowTile* tiles = reinterpret_cast<RowTile*>(tmem_slot + 2);
+  int* docs_smem = reinterpret_cast<int*>(smem + C::BODY + MAX_FLAGS + 256);   // [8 warps][TILE]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // block = ((row block, last first) * Hkv * B + (b * Hkv + hk)) * splits + split
@@ -214,8 +237,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const int b = (int)(id % a.B);
   const int rb = plan.row_blocks - 1 - (int)(id / a.B);
   const int rows = a.Sq * a.G;
-  const int n_tiles_q = plan.alternate ? 1 : 2;             // row tiles of this CTA
-  const int row0 = rb * TILE * n_tiles_q;
+  const int row0 = rb * TILE * 2;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -249,7 +271,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   {
     constexpr int CH = HD / 8;                               // 16-byte chunks of a row
     const bf16* qb = static_cast<const bf16*>(a.q) + b * a.q_batch + (long)hk * a.G * a.q_head;
-    const int total = n_tiles_q * TILE * CH;
+    const int total = 2 * TILE * CH;
     for (int c = threadIdx.x; c < total; c += NUM_THREADS) {
       const int lr = c / CH, ch = c % CH, r = row0 + lr;
       uint4 val = make_uint4(0u, 0u, 0u, 0u);
@@ -265,7 +287,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   }
   // this softmax thread's row
   const int t_own = warp >= 8 ? 1 : 0;
-  const int lr_own = ((warp & 3) * 32 + lane) + (plan.alternate ? 0 : t_own * TILE);
+  const int lr_own = (warp & 3) * 32 + lane + t_own * TILE;
   const int r_own = row0 + lr_own;
   const bool row_ok = warp >= 4 && r_own < rows;
   const int i_own = row_ok ? r_own / a.G : 0;
@@ -285,7 +307,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   __syncthreads();
 
   // ---------------- key tiles of this CTA
-  const int row_last = min(row0 + n_tiles_q * TILE, rows) - 1;
+  const int row_last = min(row0 + 2 * TILE, rows) - 1;
   const int key_end = 1 + last_key(a, seq, (long)seq.start + row_last / a.G);
   const int jt_all = (key_end + TILE - 1) / TILE;
   const int jt0 = min(split * plan.tiles_per_split, jt_all);
@@ -295,30 +317,39 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   if (listed) {
     // flags of a key tile: bit 2t = row tile t may see it, bit 2t + 1 = all of t's rows and all
     // of its keys are one document
-    for (int jt = jt0 + warp; jt < jt1; jt += NUM_THREADS / 32) {
-      int lo = INT_MAX, hi = -1;
-      bool none = false;
+    constexpr int AT_ONCE = 4;   // tiles whose loads a warp has in flight
+    for (int jq = jt0 + warp; jq < jt1; jq += AT_ONCE * (NUM_THREADS / 32)) {
+      int d[AT_ONCE][TILE / 32];
 #pragma unroll
-      for (int e = 0; e < TILE / 32; ++e) {
-        const int j = jt * TILE + e * 32 + lane;
-        const int d = j < seq.kv_len ? a.kv_doc[(long)b * a.Sk + j] : -1;
-        none |= d < 0;
-        if (d >= 0) {
-          lo = min(lo, d);
-          hi = max(hi, d);
+      for (int u = 0; u < AT_ONCE; ++u)
+#pragma unroll
+        for (int e = 0; e < TILE / 32; ++e) {
+          const int jt = jq + u * (NUM_THREADS / 32), j = jt * TILE + e * 32 + lane;
+          d[u][e] = jt < jt1 && j < seq.kv_len ? a.kv_doc[(long)b * a.Sk + j] : -1;
         }
-      }
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-      none = __any_sync(0xffffffffu, none);
-      if (lane == 0) {
-        uint8_t f = 0;
-        for (int t = 0; t < 2; ++t) {
-          const RowTile& q = tiles[t];
-          if (lo <= q.docs_hi && q.docs_lo <= hi) f |= 1u << (2 * t);
-          if (!none && !q.any_none && lo == hi && q.docs_lo == q.docs_hi && lo == q.docs_lo) f |= 2u << (2 * t);
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) {
+        const int jt = jq + u * (NUM_THREADS / 32);
+        int lo = INT_MAX, hi = -1;
+        bool none = false;
+#pragma unroll
+        for (int e = 0; e < TILE / 32; ++e) {
+          none |= d[u][e] < 0;
+          lo = min(lo, d[u][e] < 0 ? INT_MAX : d[u][e]);
+          hi = max(hi, d[u][e]);
         }
-        flags[jt - jt0] = f;
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        none = __any_sync(0xffffffffu, none);
+        if (lane == 0 && jt < jt1) {
+          uint8_t f = 0;
+          for (int t = 0; t < 2; ++t) {
+            const RowTile& q = tiles[t];
+            if (lo <= q.docs_hi && q.docs_lo <= hi) f |= 1u << (2 * t);
+            if (!none && !q.any_none && lo == hi && q.docs_lo == q.docs_hi && lo == q.docs_lo) f |= 2u << (2 * t);
+          }
+          flags[jt - jt0] = f;
+        }
       }
     }
   }
@@ -327,18 +358,17 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  // Which of the row tiles take key tile jt (bits 0 and 1); `turn` counts the tiles taken so
-  // far, by whose parity the halves alternate.
+  // Which of the row tiles take key tile jt (bits 0 and 1).
   int last_pos[2];
   bool alive[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int r_a = row0 + (plan.alternate ? 0 : t * TILE);
+    const int r_a = row0 + t * TILE;
     const int r_b = min(r_a + TILE, rows) - 1;
     alive[t] = r_a < rows;
     last_pos[t] = seq.start + max(r_b, 0) / a.G;
   }
-  auto needed = [&](int jt, int turn) -> int {
+  auto needed = [&](int jt) -> int {
     const int j0 = jt * TILE;
     int need = 0;
 #pragma unroll
@@ -347,20 +377,21 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       if (listed) n = n && ((flags[jt - jt0] >> (2 * t)) & 1);
       need |= n ? 1 << t : 0;
     }
-    if (plan.alternate && need) need = 1 << (turn & 1);
     return need;
   };
 
+  // registers: 384 x 168 at launch cover 128 x 80 + 256 x 208
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA: K and V tile of every key tile taken, in turn
-      int stage = 0, turn = 0;
+      int stage = 0;
       uint32_t phase = 0;
       long issued = 0;
       bool ok = true;
       for (int jt = jt0; jt < jt1 && ok; ++jt) {
-        if (!needed(jt, turn)) continue;
-        ++turn;
+        if (!needed(jt)) continue;
         for (int kv = 0; kv < 2; ++kv) {
           if (!ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort, WAIT_LIMIT_NS)) {
             ok = false;
@@ -389,7 +420,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     // (which overwrites that P); the other row tile's products run while t's softmax does
     const uint32_t idesc_s = ptx::idesc_bf16_f32(TILE, TILE);
     const uint32_t idesc_o = ptx::idesc_bf16_f32(TILE, HD) | (1u << 16);
-    int stage = 0, turn = 0, pend = 0, v_stage = 0, v_rows = TILE;
+    int stage = 0, pend = 0, v_stage = 0, v_rows = TILE;
     uint32_t phase = 0, v_phase = 0, p_phase[2] = {0, 0};
     bool started[2] = {false, false}, ok = true;
     auto advance = [&](int& s, uint32_t& ph) { if (++s == STAGES) { s = 0; ph ^= 1u; } };
@@ -424,11 +455,10 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     };
     for (int jt = jt0; jt <= jt1 && ok; ++jt) {
       const bool end = jt == jt1;
-      const int need = end ? 0 : needed(jt, turn);
+      const int need = end ? 0 : needed(jt);
       if (!end && !need) continue;
       int k_stage = stage;
       if (!end) {
-        ++turn;
         ok = ptx::mbar_wait_bounded(full_bar(stage), phase, abort, WAIT_LIMIT_NS);
         if (!ok) break;
         advance(stage, phase);
@@ -436,7 +466,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       ptx::tc_fence_after();
       auto qk = [&](int t) {
         if (lane == 0) {
-          const uint32_t q = sQ + (plan.alternate ? 0u : t * C::Q_BYTES), k = sKV + k_stage * C::KV_BYTES;
+          const uint32_t q = sQ + t * C::Q_BYTES, k = sKV + k_stage * C::KV_BYTES;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk)
             ptx::tc_mma_bf16(tmem_base + s_col(t), ptx::smem_desc_sw128(q + (kk >> 2) * C::HALF + (kk & 3) * 32),
@@ -478,45 +508,76 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       if (!ptx::mbar_wait_bounded(drain_bar, 0, &never, WAIT_LIMIT_NS)) record_timeout(err, abort);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax and output of row tile t_own
     const int t = t_own;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem_base + lane_addr + s_col(t), o_addr = tmem_base + lane_addr + o_col<HD>(t);
-    const bool warp_rows = (warp & 3) * 32 + row0 + (plan.alternate ? 0 : t * TILE) < rows;
+    const bool warp_rows = (warp & 3) * 32 + row0 + t * TILE < rows;
     const int p = seq.start + i_own;
     const int last = row_ok ? last_key(a, seq, (long)seq.start + i_own) : -1;
     const float slope2 = BIAS && row_ok ? a.slopes[hk * a.G + g_own] * LOG2E : 0.f;
-    const float sc = CAP ? 2.f * LOG2E * a.scale / a.cap : a.scale * LOG2E;
-    const float cap2 = CAP ? a.cap * LOG2E : 0.f;
-    float m = -INFINITY, l = 0.f;   // reference of the weights (log2 units) and their sum
+    const CapCoef cc = cap_coef(a.scale, CAP ? a.cap : 1.f);
+    // Without cap and bias the scale is applied with the reference's subtraction (one FMA), so
+    // the maximum is taken of the raw scores, signed so that the factor is positive.
+    constexpr bool RAW = !CAP && !BIAS;
+    const float sc = a.scale * LOG2E;
+    const float mul = RAW ? (sc == 0.f ? 1.f : fabsf(sc)) : 1.f;
+    const int* kdocs = docs ? a.kv_doc + (long)b * a.Sk : nullptr;
+    int* dbuf = docs_smem + (warp - 4) * TILE;
+    float m = -INFINITY;            // reference of the weights (log2 units)
+    float2 l2 = make_float2(0.f, 0.f);   // their sum
     uint32_t phase = 0;
     bool ok = true, started = false;
-    int turn = 0;
     for (int jt = jt0; jt < jt1; ++jt) {
-      const int need = needed(jt, turn);
-      if (need) ++turn;
-      if (!(need >> t & 1)) continue;
+      if (!(needed(jt) >> t & 1)) continue;
+      const int j0 = jt * TILE;
+      const bool one_doc = !docs || (listed && ((flags[jt - jt0] >> (2 * t + 1)) & 1));
+      if (!one_doc) {   // the tile's documents, staged before the scores are there
+#pragma unroll
+        for (int e = 0; e < TILE / 32; ++e) dbuf[e * 32 + lane] = kdocs[min(j0 + e * 32 + lane, a.Sk - 1)];
+        __syncwarp();
+      }
       ok = ptx::mbar_wait_bounded(s_bar(t), phase, abort, WAIT_LIMIT_NS);
       if (!ok) break;
       phase ^= 1u;
       if (warp_rows) {
         ptx::tc_fence_after();
-        const int j0 = jt * TILE;
-        const bool one_doc = !docs || (listed && ((flags[jt - jt0] >> (2 * t + 1)) & 1));
-        // scores in log2 units, masked ones -infinity
+        // scores (RAW: before their scale; else in log2 units), masked ones -infinity
         float x[TILE];
+        ptx::tmem_ld32_at<0>(s_addr, x);
+        ptx::tmem_ld32_at<32>(s_addr + 32, x);
+        ptx::tmem_ld32_at<64>(s_addr + 64, x);
+        ptx::tmem_ld32_at<96>(s_addr + 96, x);
+        ptx::tmem_ld_wait();
+        if constexpr (CAP) {
+          float far = fabsf(x[0]);
 #pragma unroll
-        for (int c = 0; c < TILE; c += 32) {
-          float v[32];
-          ptx::tmem_ld(s_addr + c, v);
-          ptx::tmem_ld_wait();
+          for (int e = 1; e < TILE; ++e) far = fmaxf(far, fabsf(x[e]));
+          if (__any_sync(0xffffffffu, !(far <= cc.limit))) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float y = CAP ? capped(v[e], sc, cap2) : v[e] * sc;
-            if (BIAS) y = fmaf(-slope2, fabsf((float)(p - (j0 + c + e))), y);
-            x[c + e] = y;
+            for (int e = 0; e < TILE; ++e) x[e] = capped_any(cc, x[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < TILE; e += 2) {
+              const float2 y = capped_poly(cc, make_float2(x[e], x[e + 1]));
+              x[e] = y.x;
+              x[e + 1] = y.y;
+            }
           }
+        } else if constexpr (RAW) {
+          if (sc <= 0.f) {
+#pragma unroll
+            for (int e = 0; e < TILE; ++e) x[e] = sc < 0.f ? -x[e] : 0.f;
+          }
+        }
+        if constexpr (BIAS) {
+          const float d0 = (float)(p - j0);
+#pragma unroll
+          for (int e = 0; e < TILE; ++e)
+            x[e] = fmaf(-slope2, fabsf(d0 - (float)e), CAP ? x[e] : x[e] * sc);
         }
         if (!__all_sync(0xffffffffu, j0 + TILE - 1 <= last || !row_ok)) {
 #pragma unroll
@@ -524,22 +585,33 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             if (j0 + e > last) x[e] = -INFINITY;
         }
         if (!one_doc) {
-          const int* kd_ = a.kv_doc + (long)b * a.Sk;
 #pragma unroll
-          for (int e = 0; e < TILE; ++e) {
-            const int d = kd_[min(j0 + e, a.Sk - 1)];
-            if (d != qdoc || qdoc < 0) x[e] = -INFINITY;
+          for (int e = 0; e < TILE; e += 4) {
+            const int4 d = *reinterpret_cast<const int4*>(dbuf + e);
+            if (d.x != qdoc) x[e] = -INFINITY;
+            if (d.y != qdoc) x[e + 1] = -INFINITY;
+            if (d.z != qdoc) x[e + 2] = -INFINITY;
+            if (d.w != qdoc) x[e + 3] = -INFINITY;
+          }
+          if (qdoc < 0) {
+#pragma unroll
+            for (int e = 0; e < TILE; ++e) x[e] = -INFINITY;
           }
         }
-        float top = x[0];
+        float t0 = fmaxf(x[0], x[1]), t1 = fmaxf(x[2], x[3]);
 #pragma unroll
-        for (int e = 1; e < TILE; ++e) top = fmaxf(top, x[e]);
+        for (int e = 4; e < TILE; e += 4) {
+          t0 = fmaxf(fmaxf(t0, x[e]), x[e + 1]);
+          t1 = fmaxf(fmaxf(t1, x[e + 2]), x[e + 3]);
+        }
+        const float top = fmaxf(t0, t1) * mul;
         // move the reference: at once while there is none, later only when it falls far behind
         const bool move = !started || top > m + RESCALE_AT;
         const float m_new = move ? fmaxf(m, top) : m;
         if (started && __any_sync(0xffffffffu, move)) {
           const float f = m_new == m ? 1.f : ex2(m - m_new);   // m = -infinity: 0
-          l *= f;
+          l2.x *= f;
+          l2.y *= f;
 #pragma unroll 1
           for (int c = 0; c < HD; c += 16) {
             float v[16];
@@ -553,14 +625,17 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         m = m_new;
         const float ref = m == -INFINITY ? 0.f : m;
+        const float2 mul2 = make_float2(mul, mul), nref2 = make_float2(-ref, -ref);
 #pragma unroll
         for (int c = 0; c < TILE; c += 32) {
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float p0 = ex2(x[c + e] - ref), p1 = ex2(x[c + e + 1] - ref);
-            l += p0 + p1;
-            w[e / 2] = bf16x2_bits(p0, p1);
+            const float2 xv = make_float2(x[c + e], x[c + e + 1]);
+            const float2 y = RAW ? __ffma2_rn(xv, mul2, nref2) : __fadd2_rn(xv, nref2);
+            const float2 pw = make_float2(ex2(y.x), ex2(y.y));
+            l2 = __fadd2_rn(l2, pw);
+            w[e / 2] = bf16x2_bits(pw.x, pw.y);
           }
           ptx::tmem_st16(s_addr + c / 2, w);
         }
@@ -571,6 +646,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(p_bar(t));
     }
+    const float l = l2.x + l2.y;
     if (ok) ok = ptx::mbar_wait_bounded(o_bar(t), 0, abort, WAIT_LIMIT_NS);
     if (!ok && !*abort) record_timeout(err, abort);
     if (ok && warp_rows) {
@@ -606,7 +682,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
       } else {
         // a part: the result over these keys and the log2 of its weight
-        const int part = plan.alternate ? 2 * split + t : split;
+        const int part = split;
         const long prow = ((long)b * a.Hkv + hk) * rows + r_own;
         const long n_rows = (long)a.B * a.Hkv * rows;
         float* o = plan.part_o + ((long)part * n_rows + prow) * HD;
@@ -635,114 +711,768 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   }
 }
 
-// Join of the parts of a row: o = sum 2^(lse - max) o_part / sum 2^(lse - max).  One warp a row.
-template <int HD>
+// ---------------------------------------------------------------- bf16, few rows: keys on the MMA's rows
+//
+// At most NR query rows (all heads of a key head, all new tokens) against a range of keys:
+//   S^T [128 keys x NR] = K Q^T,  thread = key: scores, masks, p;  P [NR][128 keys] in shared
+//   memory;  O^T [dims x NR] += V^T P^T (V as an MN-major A operand, P K-major B).
+// The row maxima cross the 128 threads by redux and shared memory; the row sums stay with the
+// threads until the end.  Bound by the K and V bytes.  Roles (192 threads): warp 0 TMA, warp
+// 1 MMA, warps 2-5 softmax and output.
+constexpr int F_THREADS = 192;
+template <int HD, int NR>
+struct FewCfg {
+  static constexpr uint32_t Q_BYTES = NR * HD * 2;
+  static constexpr uint32_t P_BYTES = NR * 256;
+  static constexpr uint32_t KV_BYTES = TILE * HD * 2;
+  static constexpr uint32_t HALF = TILE * 128;
+  // 16 rows: two CTAs an SM, so that one's set-up and last tiles run under the other's loads
+  static constexpr int NST = NR == 16 ? (HD == 128 ? 3 : 6) : (HD == 128 ? 5 : 10);
+  static constexpr size_t BODY = Q_BYTES + P_BYTES + (size_t)NST * KV_BYTES;
+  // rows' last key, position, document, slope; maxima (2 x 4 warps), references and factors (4 warps)
+  static constexpr size_t ROWS = NR * 4 * (4 + 8 + 8 + 1);
+  static constexpr size_t SMEM = 1024 + BODY + ROWS + (2 * NST + 8) * 8 + 16;
+  static constexpr uint32_t COLS = 3 * NR <= 64 ? 64 : 3 * NR <= 128 ? 128 : 256;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+template <int HD, int NR>
+__global__ void __launch_bounds__(F_THREADS, NR == 16 ? 2 : 1)
+scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ ScoredAttention a, const ScoredPlan plan, DevError* err) {
+  using C = FewCfg<HD, NR>;
+  constexpr int NST = C::NST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sQ = ptx::smem_u32(smem), sP = sQ + C::Q_BYTES, sKV = sP + C::P_BYTES;
+  uint8_t* gP = smem + C::Q_BYTES;
+  int* row_last = reinterpret_cast<int*>(smem + C::BODY);
+  int* row_pos = row_last + NR;
+  int* row_doc = row_pos + NR;
+  float* row_slope = reinterpret_cast<float*>(row_doc + NR);
+  float* wmax = row_slope + NR;           // [2][4][NR]
+  float* wref = wmax + 8 * NR;            // [4][2][NR]: a warp's references and factors
+  int* bad = reinterpret_cast<int*>(wref + 8 * NR);   // [NR]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(bad + NR);
+  const uint32_t bar0 = ptx::smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (NST + s); };
+  auto s_bar = [&](int i) { return bar0 + 8u * (2 * NST + i); };
+  const uint32_t p_bar = bar0 + 8u * (2 * NST + 2), o_bar = bar0 + 8u * (2 * NST + 3),
+                 drain_bar = bar0 + 8u * (2 * NST + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 5);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long id = blockIdx.x;
+  const int split = (int)(id % plan.splits);
+  id /= plan.splits;
+  const int hk = (int)(id % a.Hkv);
+  const int b = (int)(id / a.Hkv);
+  const int rows = a.Sq * a.G;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    ptx::mbar_init(s_bar(0), 1);
+    ptx::mbar_init(s_bar(1), 1);
+    ptx::mbar_init(p_bar, 4);
+    ptx::mbar_init(o_bar, 1);
+    ptx::mbar_init(drain_bar, 1);
+    ptx::fence_mbar_init();
+    *abort = 0;
+    ptx::tma_prefetch_desc(&tmK);
+    ptx::tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::pdl_wait();
+  ptx::pdl_trigger();
+  const SeqInfo seq = sequence_info(a, b);
+  {
+    constexpr int CH = HD / 8;
+    const bf16* qb = static_cast<const bf16*>(a.q) + b * a.q_batch + (long)hk * a.G * a.q_head;
+    for (int c = threadIdx.x; c < NR * CH; c += F_THREADS) {
+      const int r = c / CH, ch = c % CH;
+      uint4 val = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) {
+        const int i = r / a.G, g = r - i * a.G;
+        val = *reinterpret_cast<const uint4*>(qb + i * a.q_token + g * a.q_head + ch * 8);
+      }
+      *reinterpret_cast<uint4*>(smem + (ch >> 3) * (NR * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = val;
+    }
+    ptx::fence_proxy_async_smem();
+    for (int r = threadIdx.x; r < NR; r += F_THREADS) {
+      const bool ok = r < rows;
+      const int i = ok ? r / a.G : 0, g = ok ? r - i * a.G : 0;
+      row_last[r] = ok ? last_key(a, seq, (long)seq.start + i) : -1;
+      row_pos[r] = seq.start + i;
+      row_doc[r] = ok && a.q_doc ? a.q_doc[(long)b * a.Sq + i] : 0;
+      row_slope[r] = ok && a.slopes ? a.slopes[hk * a.G + g] * LOG2E : 0.f;
+      bad[r] = 0;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  // keys of this CTA: up to the last one that any row sees (the last token's)
+  const int key_end = 1 + row_last[rows - 1];
+  const int jt_all = (key_end + TILE - 1) / TILE;
+  const int jt0 = min(split * plan.tiles_per_split, jt_all), jt1 = min(jt0 + plan.tiles_per_split, jt_all);
+  const int n_tiles = jt1 - jt0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      long issued = 0;
+      for (int n = 0; n < 2 * n_tiles; ++n) {
+        ok = ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort, WAIT_LIMIT_NS);
+        if (!ok) break;
+        ptx::mbar_arrive_expect_tx(full_bar(stage), C::KV_BYTES);
+#pragma unroll
+        for (int hf = 0; hf < HD / 64; ++hf)
+          ptx::tma_load_4d(sKV + stage * C::KV_BYTES + hf * C::HALF, n & 1 ? &tmV : &tmK, full_bar(stage), hf * 64,
+                           (jt0 + (n >> 1)) * TILE, hk, b);
+        ++issued;
+        if (++stage == NST) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok && !*abort) record_timeout(err, abort);
+      // every copy issued has landed before the CTA leaves
+      const long n = issued < NST ? issued : NST;
+      volatile int never = 0;
+      for (long i = 0; i < n; ++i) {
+        if (--stage < 0) { stage = NST - 1; phase ^= 1u; }
+        ptx::mbar_wait_bounded(full_bar(stage), phase, &never, WAIT_LIMIT_NS);
+      }
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc_s = ptx::idesc_bf16_f32(TILE, NR);
+    const uint32_t idesc_o = ptx::idesc_bf16_f32(TILE, NR) | (1u << 15);
+    // 64 dims: both 64-row halves of the MMA read the same values, the second half is not used
+    constexpr uint32_t V_ATOM = HD == 128 ? C::HALF : 0u;
+    bool ok = true;
+    auto stage_of = [](int i) { return i % NST; };
+    auto phase_of = [](int i) { return (uint32_t)((i / NST) & 1); };
+    auto qk = [&](int n) {   // S^T of tile n into buffer n & 1, whose last use P V of tile n - 2 precedes
+      ok = ptx::mbar_wait_bounded(full_bar(stage_of(2 * n)), phase_of(2 * n), abort, WAIT_LIMIT_NS);
+      if (!ok) return;
+      ptx::tc_fence_after();
+      if (lane == 0) {
+        const uint32_t k = sKV + stage_of(2 * n) * C::KV_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          ptx::tc_mma_bf16(tmem_base + (n & 1) * NR, ptx::smem_desc_sw128(k + (kk >> 2) * C::HALF + (kk & 3) * 32),
+                           ptx::smem_desc_sw128(sQ + (kk >> 2) * (NR * 128) + (kk & 3) * 32), idesc_s, kk != 0);
+        ptx::tc_commit(empty_bar(stage_of(2 * n)));
+        ptx::tc_commit(s_bar(n & 1));
+      }
+      __syncwarp();
+    };
+    if (n_tiles > 0) qk(0);
+    for (int n = 0; n < n_tiles && ok; ++n) {
+      if (n + 1 < n_tiles) qk(n + 1);
+      const int vs = stage_of(2 * n + 1);
+      if (ok) ok = ptx::mbar_wait_bounded(full_bar(vs), phase_of(2 * n + 1), abort, WAIT_LIMIT_NS);
+      if (!ok) break;
+      const int v_rows = min(seq.kv_len - (jt0 + n) * TILE, TILE);
+      if (v_rows < TILE) {   // value rows past the last key: 0, whatever they hold
+        uint8_t* v = smem + C::Q_BYTES + C::P_BYTES + (size_t)vs * C::KV_BYTES;
+        const int cnt = (TILE - v_rows) * 8;
+        for (int c = lane; c < cnt * (HD / 64); c += 32) {
+          const int hf = c / cnt, e = c % cnt;
+          *reinterpret_cast<uint4*>(v + hf * C::HALF + (v_rows + e / 8) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+      }
+      ok = ptx::mbar_wait_bounded(p_bar, n & 1, abort, WAIT_LIMIT_NS);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (lane == 0) {
+        const uint32_t v = sKV + vs * C::KV_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < TILE / 16; ++kk)
+          ptx::tc_mma_bf16(tmem_base + 2 * NR, desc_mn(v + kk * 2048, V_ATOM),
+                           ptx::smem_desc_sw128(sP + (kk >> 2) * (NR * 128) + (kk & 3) * 32), idesc_o, (n | kk) != 0);
+        ptx::tc_commit(empty_bar(vs));
+        ptx::tc_commit(o_bar);
+      }
+      __syncwarp();
+    }
+    if (!ok && !*abort && lane == 0) record_timeout(err, abort);
+    if (lane == 0) {
+      ptx::tc_commit(drain_bar);
+      volatile int never = 0;
+      if (!ptx::mbar_wait_bounded(drain_bar, 0, &never, WAIT_LIMIT_NS)) record_timeout(err, abort);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax: this thread's key of the tile, then this thread's dim of the output
+    const int quarter = warp & 3, sw = warp - 2, key = quarter * 32 + lane;
+    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t o_addr = tmem_base + lane_addr + 2 * NR;
+    constexpr int RL = (NR + 31) / 32;          // rows kept per lane
+    const bool cap = a.cap > 0.f, bias = a.slopes != nullptr, docs = a.q_doc != nullptr;
+    const CapCoef cc = cap_coef(a.scale, cap ? a.cap : 1.f);
+    const float sc = a.scale * LOG2E;
+    const int all_see = row_last[0];            // keys up to here are seen by every row
+    float* refs = wref + sw * 2 * NR;
+    float* facs = refs + NR;
+    float my_ref[RL], l[NR];
+#pragma unroll
+    for (int c = 0; c < RL; ++c) my_ref[c] = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) l[r] = 0.f;
+    bool ok = true;
+    for (int n = 0; n < n_tiles; ++n) {
+      const int j = (jt0 + n) * TILE + key;
+      const int kd = docs ? a.kv_doc[(long)b * a.Sk + min(j, a.Sk - 1)] : 0;
+      ok = ptx::mbar_wait_bounded(s_bar(n & 1), (n >> 1) & 1, abort, WAIT_LIMIT_NS);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      float x[NR];
+      const uint32_t s_addr = tmem_base + lane_addr + (n & 1) * NR;
+      ptx::tmem_ld16_at<0>(s_addr, x);
+      if constexpr (NR > 16) ptx::tmem_ld16_at<NR - 16>(s_addr + NR - 16, x);
+      if constexpr (NR > 32) {
+        ptx::tmem_ld16_at<16>(s_addr + 16, x);
+        ptx::tmem_ld16_at<NR - 32>(s_addr + NR - 32, x);
+      }
+      ptx::tmem_ld_wait();
+      if (cap) {
+        float far = 0.f;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) far = fmaxf(far, fabsf(x[r]));
+        if (__any_sync(0xffffffffu, !(far <= cc.limit))) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) x[r] = capped_any(cc, x[r]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < NR; r += 2) {
+            const float2 y = capped_poly(cc, make_float2(x[r], x[r + 1]));
+            x[r] = y.x;
+            x[r + 1] = y.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) x[r] *= sc;
+      }
+      if (bias) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) x[r] = fmaf(-row_slope[r], fabsf((float)(row_pos[r] - j)), x[r]);
+      }
+      if ((jt0 + n) * TILE + TILE - 1 > all_see) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          if (j > row_last[r]) x[r] = -INFINITY;
+      }
+      if (docs) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          if (kd < 0 || row_doc[r] != kd) x[r] = -INFINITY;
+      }
+      // row maxima over the tile: within the warp, then over the four
+      float* wm = wmax + (n & 1) * 4 * NR;
+#pragma unroll
+      for (int c = 0; c < RL; ++c) {
+        float keep = -INFINITY;
+#pragma unroll
+        for (int r = 32 * c; r < 32 * c + 32 && r < NR; ++r) {
+          const float v = warp_max(x[r]);
+          if (lane == (r & 31)) keep = v;
+        }
+        if (32 * c + lane < NR) wm[sw * NR + 32 * c + lane] = keep;
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      bool any = false;
+#pragma unroll
+      for (int c = 0; c < RL; ++c) {
+        const int r = 32 * c + lane;
+        if (r < NR) {
+          const float top = fmaxf(fmaxf(wm[r], wm[NR + r]), fmaxf(wm[2 * NR + r], wm[3 * NR + r]));
+          const bool move = n == 0 || top > my_ref[c] + RESCALE_AT;
+          const float next = move ? fmaxf(my_ref[c], top) : my_ref[c];
+          facs[r] = next == my_ref[c] ? 1.f : ex2(my_ref[c] - next);
+          any |= move;
+          my_ref[c] = next;
+          refs[r] = next == -INFINITY ? 0.f : next;
+        }
+      }
+      any = __any_sync(0xffffffffu, any);   // the same in all four warps
+      __syncwarp();
+      if (n > 0) {
+        ok = ptx::mbar_wait_bounded(o_bar, (n - 1) & 1, abort, WAIT_LIMIT_NS);   // P and O of tile n - 1
+        if (!ok) break;
+        if (any) {
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < NR; c += 16) {
+            float v[16];
+            uint32_t w[16];
+            ptx::tmem_ld(o_addr + c, v);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              w[e] = __float_as_uint(v[e] * facs[c + e]);
+              l[c + e] *= facs[c + e];
+            }
+            ptx::tmem_st16(o_addr + c, w);
+          }
+          ptx::tmem_st_wait();
+        }
+      }
+      // weights: P row r, this key (K-major, 128-byte swizzle, 64 keys a block)
+      uint8_t* pk = gP + (key >> 6) * (NR * 128) + (key & 7) * 2;
+      const int ch = (key & 63) >> 3;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float w = ex2(x[r] - refs[r]);
+        l[r] += w;
+        *reinterpret_cast<bf16*>(pk + r * 128 + ((ch ^ (r & 7)) << 4)) = __float2bfloat16_rn(w);
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(p_bar);
+    }
+    // row sums over the threads: in the warp, then over the four (the maxima's first buffer)
+    if (n_tiles > 0 && ok) ok = ptx::mbar_wait_bounded(o_bar, (n_tiles - 1) & 1, abort, WAIT_LIMIT_NS);
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      float v = l[r];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == (r & 31)) wmax[sw * NR + r] = v;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (!ok && !*abort) record_timeout(err, abort);
+    if (ok) {
+      ptx::tc_fence_after();
+      const long n_rows = (long)a.B * a.Hkv * rows, prow = ((long)b * a.Hkv + hk) * rows;
+      const int d = quarter * 32 + lane;       // output dim (HD 64: quarters 0 and 1)
+      if (plan.parts > 1) {
+        for (int r = threadIdx.x - 64; r < rows; r += 128) {
+          const float sum = wmax[r] + wmax[NR + r] + wmax[2 * NR + r] + wmax[3 * NR + r];
+          const float ref = wref[r];           // any warp's copy
+          plan.part_lse[(long)split * n_rows + prow + r] = n_tiles > 0 && sum != 0.f ? ref + log2f(sum) : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < NR; c += 16) {
+        if (c < rows) {
+          float v[16];
+          ptx::tmem_ld(o_addr + c, v);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int r = c + e;
+            if (r < rows && d < HD) {
+              const float sum = wmax[r] + wmax[NR + r] + wmax[2 * NR + r] + wmax[3 * NR + r];
+              const bool seen = n_tiles > 0 && sum != 0.f;
+              const float y = seen ? v[e] / sum : 0.f;
+              if (plan.parts > 1) {
+                if (seen) plan.part_o[((long)split * n_rows + prow + r) * HD + d] = y;
+              } else {
+                const int i = r / a.G, g = r - i * a.G;
+                static_cast<bf16*>(a.out)[b * a.o_batch + i * a.o_token + (long)(hk * a.G + g) * a.o_head + d] =
+                    __float2bfloat16_rn(y);
+                if (!(fabsf(y) < INFINITY)) bad[r] = 1;
+              }
+            }
+          }
+        }
+      }
+      if (plan.parts == 1) {
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        for (int r = sw; r < rows; r += 4)
+          if (bad[r]) row_by_warp<bf16, HD>(a, b, hk * a.G + r % a.G, r / a.G);
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, C::COLS);
+  }
+}
+
+// ---------------------------------------------------------------- fp32
+//
+// The fp32 path on the FMA units (the tensor cores have no fp32 kind, and tf32 rounds too
+// much).  A CTA of 128 threads takes 16 * TM rows and walks key tiles of 32: thread (row
+// group, column group) holds TM x 4 scores and TM x HD / 8 outputs in registers; keys, values,
+// queries and weights pass through shared memory, rows padded by 16 bytes so that the
+// column groups of a warp read different banks.  A row's statistics live in the 8 lanes that
+// share it.  TM = 4 for many rows, 1 where at most 16 would leave the rest idle.
+constexpr int FT = 32;                       // keys of a tile
+template <int HD, int TM>
+struct F32Cfg {
+  static constexpr int BM = 16 * TM, LD = HD + 4, LP = FT + 4;
+  static constexpr size_t SMEM = (size_t)(BM * LD + 2 * FT * LD + BM * LP) * 4;
+};
+
+template <int HD, int TM>
+__global__ void __launch_bounds__(128) scored_f32_kernel(const __grid_constant__ ScoredAttention a,
+                                                         const ScoredPlan plan) {
+  using C = F32Cfg<HD, TM>;
+  constexpr int BM = C::BM, LD = C::LD, LP = C::LP, ND = HD / 32;   // float4 of outputs per row and thread
+  extern __shared__ float fsm[];
+  float* sQ = fsm;
+  float* sK = sQ + BM * LD;
+  float* sV = sK + FT * LD;
+  float* sP = sV + FT * LD;
+  ptx::pdl_wait();
+  ptx::pdl_trigger();
+  long id = blockIdx.x;
+  const int split = (int)(id % plan.splits);
+  id /= plan.splits;
+  const int hk = (int)(id % a.Hkv);
+  id /= a.Hkv;
+  const int b = (int)(id % a.B);
+  const int rb = plan.row_blocks - 1 - (int)(id / a.B);
+  const int rows = a.Sq * a.G, row0 = rb * BM;
+  const SeqInfo seq = sequence_info(a, b);
+  const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;            // column group, row group (16)
+  const int row_end = min(row0 + BM, rows);
+
+  const float* qb = static_cast<const float*>(a.q) + b * a.q_batch + (long)hk * a.G * a.q_head;
+  for (int c = threadIdx.x; c < BM * (HD / 4); c += 128) {
+    const int lr = c / (HD / 4), ch = c % (HD / 4), r = row0 + lr;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) {
+      const int i = r / a.G, g = r - i * a.G;
+      v = *reinterpret_cast<const float4*>(qb + i * a.q_token + g * a.q_head + ch * 4);
+    }
+    *reinterpret_cast<float4*>(sQ + lr * LD + ch * 4) = v;
+  }
+  // row u of this thread: local row rg + 16 u (so that a warp's four rows differ in banks)
+  int last[TM], pos[TM], doc[TM];
+  float slope[TM], m[TM], l[TM];
+  float4 o[TM][ND];
+#pragma unroll
+  for (int u = 0; u < TM; ++u) {
+    const int r = row0 + rg + 16 * u;
+    const bool ok = r < rows;
+    const int i = ok ? r / a.G : 0, g = ok ? r - i * a.G : 0;
+    pos[u] = seq.start + i;
+    last[u] = ok ? last_key(a, seq, (long)seq.start + i) : -1;
+    doc[u] = ok && a.q_doc ? a.q_doc[(long)b * a.Sq + i] : 0;
+    slope[u] = ok && a.slopes ? a.slopes[hk * a.G + g] * LOG2E : 0.f;
+    m[u] = -INFINITY;
+    l[u] = 0.f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[u][d] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const int key_end = 1 + last_key(a, seq, (long)seq.start + (row_end - 1) / a.G);
+  const int jt_all = (key_end + FT - 1) / FT;
+  const int jt0 = min(split * plan.tiles_per_split, jt_all), jt1 = min(jt0 + plan.tiles_per_split, jt_all);
+  const bool docs = a.q_doc != nullptr;
+  const float* kb = static_cast<const float*>(a.k) + b * a.k_batch + hk * a.k_head;
+  const float* vb = static_cast<const float*>(a.v) + b * a.v_batch + hk * a.v_head;
+  for (int jt = jt0; jt < jt1; ++jt) {
+    const int j0 = jt * FT;
+    __syncthreads();
+    for (int c = threadIdx.x; c < FT * (HD / 4); c += 128) {
+      const int lj = c / (HD / 4), ch = c % (HD / 4), j = j0 + lj;
+      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+      if (j < seq.kv_len) {
+        kv = *reinterpret_cast<const float4*>(kb + j * a.k_token + ch * 4);
+        vv = *reinterpret_cast<const float4*>(vb + j * a.v_token + ch * 4);
+      }
+      *reinterpret_cast<float4*>(sK + lj * LD + ch * 4) = kv;
+      *reinterpret_cast<float4*>(sV + lj * LD + ch * 4) = vv;
+    }
+    __syncthreads();
+    // scores of keys cg + 8 w
+    float2 acc[TM][4];
+#pragma unroll
+    for (int u = 0; u < TM; ++u)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) acc[u][w] = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int d = 0; d < HD; d += 4) {
+      float4 q4[TM], k4[4];
+#pragma unroll
+      for (int u = 0; u < TM; ++u) q4[u] = *reinterpret_cast<const float4*>(sQ + (rg + 16 * u) * LD + d);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) k4[w] = *reinterpret_cast<const float4*>(sK + (cg + 8 * w) * LD + d);
+#pragma unroll
+      for (int u = 0; u < TM; ++u)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          acc[u][w] = __ffma2_rn(make_float2(q4[u].x, q4[u].y), make_float2(k4[w].x, k4[w].y), acc[u][w]);
+          acc[u][w] = __ffma2_rn(make_float2(q4[u].z, q4[u].w), make_float2(k4[w].z, k4[w].w), acc[u][w]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < TM; ++u) {
+      float x[4], top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int j = j0 + cg + 8 * w;
+        float y = (acc[u][w].x + acc[u][w].y) * a.scale;
+        y = a.cap > 0.f ? a.cap * tanhf(y / a.cap) * LOG2E : y * LOG2E;
+        if (a.slopes) y = fmaf(-slope[u], fabsf((float)(pos[u] - j)), y);
+        bool seen = j <= last[u];
+        if (docs && seen) seen = doc[u] >= 0 && a.kv_doc[(long)b * a.Sk + j] == doc[u];
+        x[w] = seen ? y : -INFINITY;
+        top = fmaxf(top, x[w]);
+      }
+#pragma unroll
+      for (int s = 1; s < 8; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      const float mn = fmaxf(m[u], top), ref = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m[u] - ref);
+      m[u] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float p = exp2f(x[w] - ref);
+        sum += p;
+        sP[(rg + 16 * u) * LP + cg + 8 * w] = p;
+      }
+      l[u] = l[u] * f + sum;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        o[u][d].x *= f; o[u][d].y *= f; o[u][d].z *= f; o[u][d].w *= f;
+      }
+    }
+    __syncwarp();   // a row's weights are read by the 8 lanes that wrote them
+    // outputs: dims 4 cg + 32 d
+#pragma unroll 2
+    for (int j = 0; j < FT; j += 4) {
+      float4 p4[TM];
+#pragma unroll
+      for (int u = 0; u < TM; ++u) p4[u] = *reinterpret_cast<const float4*>(sP + (rg + 16 * u) * LP + j);
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const float4 v = *reinterpret_cast<const float4*>(sV + (j + w) * LD + 32 * d + 4 * cg);
+#pragma unroll
+          for (int u = 0; u < TM; ++u) {
+            const float p = w == 0 ? p4[u].x : w == 1 ? p4[u].y : w == 2 ? p4[u].z : p4[u].w;
+            float2 lo = __ffma2_rn(make_float2(p, p), make_float2(v.x, v.y), make_float2(o[u][d].x, o[u][d].y));
+            float2 hi = __ffma2_rn(make_float2(p, p), make_float2(v.z, v.w), make_float2(o[u][d].z, o[u][d].w));
+            o[u][d] = make_float4(lo.x, lo.y, hi.x, hi.y);
+          }
+        }
+    }
+  }
+  const long n_rows = (long)a.B * a.Hkv * rows, prow = ((long)b * a.Hkv + hk) * rows;
+#pragma unroll
+  for (int u = 0; u < TM; ++u) {
+    const int r = row0 + rg + 16 * u;
+    const bool row_ok = r < rows;
+    float sum = l[u];
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    const bool seen = sum != 0.f;
+    const int i = row_ok ? r / a.G : 0, g = row_ok ? r - i * a.G : 0;
+    bool finite = true;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      const float4 y = seen ? make_float4(o[u][d].x / sum, o[u][d].y / sum, o[u][d].z / sum, o[u][d].w / sum)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+      finite = finite && fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY && fabsf(y.z) < INFINITY && fabsf(y.w) < INFINITY;
+      if (row_ok) {
+        if (plan.parts == 1)
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + b * a.o_batch + i * a.o_token +
+                                     (long)(hk * a.G + g) * a.o_head + 32 * d + 4 * cg) = y;
+        else if (seen)
+          *reinterpret_cast<float4*>(plan.part_o + ((long)split * n_rows + prow + r) * HD + 32 * d + 4 * cg) = y;
+      }
+    }
+    if (plan.parts == 1) {
+      unsigned redo = __ballot_sync(0xffffffffu, row_ok && !finite);
+      while (redo) {
+        const int src = __ffs(redo) - 1;
+        redo &= ~(0xffu << (src & ~7));     // the 8 lanes of that row
+        row_by_warp<float, HD>(a, b, hk * a.G + __shfl_sync(0xffffffffu, g, src), __shfl_sync(0xffffffffu, i, src));
+      }
+    } else if (row_ok && cg == 0) {
+      plan.part_lse[(long)split * n_rows + prow + r] = seen ? m[u] + log2f(sum) : -INFINITY;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- join of the parts
+// o = sum 2^(lse - max) o_part / sum 2^(lse - max).  One CTA a row: warp w takes parts w, w + 4, ...
+template <typename T, int HD>
 __global__ void __launch_bounds__(128) scored_join_kernel(const __grid_constant__ ScoredAttention a,
                                                           const ScoredPlan plan) {
   constexpr int PER = HD / 32;
+  __shared__ float sm[4], st[4], so[4][HD];
   ptx::pdl_wait();
   ptx::pdl_trigger();
   const int rows = a.Sq * a.G;
   const long n_rows = (long)a.B * a.Hkv * rows;
-  const long r = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (r >= n_rows) return;
-  const int lane = threadIdx.x & 31;
+  const long r = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float top = -INFINITY;
-  for (int s = lane; s < plan.parts; s += 32) top = fmaxf(top, plan.part_lse[s * n_rows + r]);
+  for (int s = threadIdx.x; s < plan.parts; s += 128) top = fmaxf(top, plan.part_lse[s * n_rows + r]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) sm[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
   const float ref = top == -INFINITY ? 0.f : top;
   float total = 0.f, o[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) o[e] = 0.f;
-  for (int s = 0; s < plan.parts; ++s) {
-    const float lse = plan.part_lse[s * n_rows + r];
-    if (lse == -INFINITY) continue;
-    const float w = exp2f(lse - ref);
-    total += w;
-    const float* po = plan.part_o + (s * n_rows + r) * HD + lane * PER;
+#pragma unroll 4
+  for (int s = warp; s < plan.parts; s += 4) {
+    const float w = exp2f(plan.part_lse[s * n_rows + r] - ref);
+    float v[PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = fmaf(w, po[e], o[e]);
+    for (int e = 0; e < PER; ++e) v[e] = 0.f;
+    if (w != 0.f) {   // a part that saw nothing has no values
+      const float* po = plan.part_o + (s * n_rows + r) * HD + lane * PER;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) v[e] = po[e];
+    }
+    total += w;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = fmaf(w, v[e], o[e]);
   }
+  if (lane == 0) st[warp] = total;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) so[warp][lane * PER + e] = o[e];
+  __syncthreads();
+  if (warp != 0) return;
+  total = st[0] + st[1] + st[2] + st[3];
   const int rr = (int)(r % rows), i = rr / a.G, g = rr - i * a.G;
   const int bh = (int)(r / rows), hk = bh % a.Hkv, b = bh / a.Hkv, hq = hk * a.G + g;
-  bf16* out = static_cast<bf16*>(a.out) + b * a.o_batch + i * a.o_token + hq * a.o_head + lane * PER;
+  T* out = static_cast<T*>(a.out) + b * a.o_batch + i * a.o_token + hq * a.o_head + lane * PER;
   bool finite = true;
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
-    const float y = total == 0.f ? 0.f : o[e] / total;
+    const int d = lane * PER + e;
+    const float y = total == 0.f ? 0.f : (so[0][d] + so[1][d] + so[2][d] + so[3][d]) / total;
     finite = finite && fabsf(y) < INFINITY;
-    out[e] = __float2bfloat16_rn(y);
+    out[e] = from_f<T>(y);
   }
-  if (!__all_sync(0xffffffffu, finite)) row_by_warp<bf16, HD>(a, b, hq, i);
+  if (!__all_sync(0xffffffffu, finite)) row_by_warp<T, HD>(a, b, hq, i);
 }
 
-template <int HD, bool CAP, bool BIAS>
-cudaError_t launch_tc(const ScoredAttention& a, const ScoredPlan& plan, DevError* err, cudaStream_t st) {
-  using C = Cfg<HD>;
-  auto kern = scored_tc_kernel<HD, CAP, BIAS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+// ---------------------------------------------------------------- host side
+
+template <typename T, int HD>
+cudaError_t join(const ScoredAttention& a, const ScoredPlan& plan, cudaStream_t st) {
+  if (plan.parts == 1) return cudaSuccess;
+  const long n_rows = (long)a.B * a.Hq * a.Sq;
+  return launch_kernel(scored_join_kernel<T, HD>, dim3((unsigned)n_rows), dim3(128), 0, st, a, plan);
+}
+
+template <typename K>
+cudaError_t launch_maps(K kern, int threads, size_t smem, const ScoredAttention& a, const ScoredPlan& plan,
+                        DevError* err, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   CUtensorMap tk, tv;
   // without keys no copy is issued; the maps then describe one token of q
   const bool keys = a.Sk > 0;
   const int tokens = keys ? a.Sk : 1;
-  if (make_tmap_heads(&tk, keys ? a.k : a.q, HD, tokens, a.Hkv, a.B, a.k_token, a.k_head, a.k_batch) ||
-      make_tmap_heads(&tv, keys ? a.v : a.q, HD, tokens, a.Hkv, a.B, a.v_token, a.v_head, a.v_batch))
+  if (make_tmap_heads(&tk, keys ? a.k : a.q, a.HD, tokens, a.Hkv, a.B, a.k_token, a.k_head, a.k_batch) ||
+      make_tmap_heads(&tv, keys ? a.v : a.q, a.HD, tokens, a.Hkv, a.B, a.v_token, a.v_head, a.v_batch))
     return cudaErrorInvalidValue;
   const long grid = (long)plan.row_blocks * a.Hkv * a.B * plan.splits;
   if (grid > INT_MAX) return cudaErrorInvalidValue;
-  e = launch_kernel(kern, dim3((unsigned)grid), dim3(NUM_THREADS), C::SMEM, st, tk, tv, a, plan, err);
-  if (e != cudaSuccess || plan.parts == 1) return e;
-  const long n_rows = (long)a.B * a.Hq * a.Sq;
-  return launch_kernel(scored_join_kernel<HD>, dim3((unsigned)((n_rows + 3) / 4)), dim3(128), 0, st, a, plan);
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(threads), smem, st, tk, tv, a, plan, err);
 }
 
 template <int HD>
 cudaError_t run_tc(const ScoredAttention& a, const ScoredPlan& plan, DevError* err, cudaStream_t st) {
-  if (a.cap > 0.f)
-    return a.slopes ? launch_tc<HD, true, true>(a, plan, err, st) : launch_tc<HD, true, false>(a, plan, err, st);
-  return a.slopes ? launch_tc<HD, false, true>(a, plan, err, st) : launch_tc<HD, false, false>(a, plan, err, st);
+  const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
+  cudaError_t e;
+  if (plan.few == 16)
+    e = launch_maps(scored_few_kernel<HD, 16>, F_THREADS, FewCfg<HD, 16>::SMEM, a, plan, err, st);
+  else if (plan.few == 32)
+    e = launch_maps(scored_few_kernel<HD, 32>, F_THREADS, FewCfg<HD, 32>::SMEM, a, plan, err, st);
+  else if (plan.few == 64)
+    e = launch_maps(scored_few_kernel<HD, 64>, F_THREADS, FewCfg<HD, 64>::SMEM, a, plan, err, st);
+  else if (cap)
+    e = bias ? launch_maps(scored_tc_kernel<HD, true, true>, NUM_THREADS, Cfg<HD>::SMEM, a, plan, err, st)
+             : launch_maps(scored_tc_kernel<HD, true, false>, NUM_THREADS, Cfg<HD>::SMEM, a, plan, err, st);
+  else
+    e = bias ? launch_maps(scored_tc_kernel<HD, false, true>, NUM_THREADS, Cfg<HD>::SMEM, a, plan, err, st)
+             : launch_maps(scored_tc_kernel<HD, false, false>, NUM_THREADS, Cfg<HD>::SMEM, a, plan, err, st);
+  return e != cudaSuccess ? e : join<bf16, HD>(a, plan, st);
+}
+
+template <int HD, int TM>
+cudaError_t launch_f32(const ScoredAttention& a, const ScoredPlan& plan, cudaStream_t st) {
+  using C = F32Cfg<HD, TM>;
+  auto kern = scored_f32_kernel<HD, TM>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long grid = (long)plan.row_blocks * a.Hkv * a.B * plan.splits;
+  if (grid > INT_MAX) return cudaErrorInvalidValue;
+  e = launch_kernel(kern, dim3((unsigned)grid), dim3(128), C::SMEM, st, a, plan);
+  return e != cudaSuccess ? e : join<float, HD>(a, plan, st);
 }
 
 }  // namespace
 
-// How a bf16 call is laid out over the GPU.  At most 128 rows a key head leave one row tile,
-// whose key tiles the two halves of a CTA take in turn; keys are split further while the
-// CTAs do not fill the SMs and every part keeps two tiles.
-ScoredPlan scored_attention_plan(const ScoredAttention& a, int num_sms) {
+// How a call is laid out over the GPU: row blocks by the number of rows a key head has, and
+// keys split while the CTAs do not fill the SMs (`fill` CTAs an SM) and every part keeps
+// `least` key tiles.
+ScoredPlan scored_attention_plan(const ScoredAttention& a, bool is_bf16, int num_sms) {
   ScoredPlan p;
   const long rows = (long)a.Sq * a.G;
-  const int key_tiles = (a.Sk + TILE - 1) / TILE;
-  p.alternate = rows <= TILE && key_tiles > 1;
-  p.row_blocks = (int)((rows + 2 * TILE - 1) / (2 * TILE));
-  const long ctas = (long)p.row_blocks * a.Hkv * a.B;
-  long splits = ctas < num_sms ? num_sms / ctas : 1;
-  if (splits > (key_tiles + 1) / 2) splits = (key_tiles + 1) / 2;
+  int block, tile, fill, least;
+  if (is_bf16) {
+    p.few = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
+    block = p.few ? p.few : 2 * TILE;
+    tile = TILE;
+    fill = p.few ? 4 : 1;
+    least = 2;
+  } else {
+    p.few = rows <= 16 ? 16 : 0;
+    block = p.few ? 16 : 64;
+    tile = FT;
+    fill = 3;
+    least = 4;
+  }
+  p.row_blocks = (int)((rows + block - 1) / block);
+  const int key_tiles = (a.Sk + tile - 1) / tile;
+  const long ctas = (long)p.row_blocks * a.Hkv * a.B, want = (long)fill * num_sms;
+  long splits = ctas < want ? want / ctas : 1;
+  if (splits > key_tiles / least) splits = key_tiles / least;
   if (splits < 1) splits = 1;
   p.tiles_per_split = (int)((key_tiles + splits - 1) / splits);
   if (p.tiles_per_split < 1) p.tiles_per_split = 1;
   p.splits = key_tiles > 0 ? (key_tiles + p.tiles_per_split - 1) / p.tiles_per_split : 1;
-  p.parts = p.splits * (p.alternate ? 2 : 1);
-  const long n_rows = (long)a.B * a.Hkv * rows;
-  p.bytes = p.parts > 1 ? (size_t)p.parts * n_rows * (a.HD + 1) * 4 : 0;
+  p.parts = p.splits;
+  p.bytes = p.parts > 1 ? (size_t)p.parts * a.B * a.Hkv * rows * (a.HD + 1) * 4 : 0;
   return p;
 }
 
-cudaError_t attention_scored_bf16(const ScoredAttention& a, ScoredPlan plan, void* workspace, DevError* err,
-                                  cudaStream_t st) {
+cudaError_t attention_scored(const ScoredAttention& a, bool is_bf16, ScoredPlan plan, void* workspace, DevError* err,
+                             cudaStream_t st) {
   if (plan.parts > 1) {
     plan.part_o = static_cast<float*>(workspace);
     plan.part_lse = plan.part_o + (size_t)plan.parts * a.B * a.Hq * a.Sq * a.HD;
   }
-  return a.HD == 64 ? run_tc<64>(a, plan, err, st) : run_tc<128>(a, plan, err, st);
-}
-
-cudaError_t attention_scored_f32(const ScoredAttention& a, cudaStream_t st) {
-  const long rows = (long)a.B * a.Sq * a.Hq;
-  const dim3 grid((unsigned)((rows + 3) / 4));
-  return a.HD == 64 ? launch_kernel(scored_f32_kernel<64>, grid, dim3(128), 0, st, a)
-                    : launch_kernel(scored_f32_kernel<128>, grid, dim3(128), 0, st, a);
+  if (is_bf16) return a.HD == 64 ? run_tc<64>(a, plan, err, st) : run_tc<128>(a, plan, err, st);
+  if (plan.few)
+    return a.HD == 64 ? launch_f32<64, 1>(a, plan, st) : launch_f32<128, 1>(a, plan, st);
+  return a.HD == 64 ? launch_f32<64, 4>(a, plan, st) : launch_f32<128, 4>(a, plan, st);
 }
 
 }  // namespace kd

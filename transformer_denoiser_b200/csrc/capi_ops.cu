@@ -169,6 +169,8 @@ int scored_args(const kimodo_scored_attention* p, ScoredAttention* a) {
     return set_error(KIMODO_EINVAL, "too many query rows");
   if (!isfinite(p->scale)) return set_error(KIMODO_EINVAL, "scale must be finite");
   if (!isfinite(p->cap) || p->cap < 0.f) return set_error(KIMODO_EINVAL, "cap must be finite and >= 0");
+  if (p->cap > 0.f && !(fabsf(p->scale) <= 1e6f * p->cap))
+    return set_error(KIMODO_EINVAL, "cap must be at least a millionth of the scale");
   if (p->prefix && !p->causal) return set_error(KIMODO_EINVAL, "prefix needs causal");
   if ((p->q_documents == nullptr) != (p->kv_documents == nullptr))
     return set_error(KIMODO_EINVAL, "q_documents and kv_documents come together");
@@ -217,10 +219,9 @@ int kimodo_attention_scored_workspace(const kimodo_scored_attention* args, size_
   *bytes = 0;
   ScoredAttention a;
   KD_TRY(scored_args(args, &a));
-  if (args->dtype != KIMODO_BF16) return KIMODO_OK;
   const int sms = current_sms();
   if (sms < 1) return set_error(KIMODO_EUNSUPPORTED, "no CUDA device available");
-  *bytes = scored_attention_plan(a, sms).bytes;
+  *bytes = scored_attention_plan(a, args->dtype == KIMODO_BF16, sms).bytes;
   return KIMODO_OK;
 }
 
@@ -231,14 +232,11 @@ int kimodo_attention_scored(const kimodo_scored_attention* args, void* workspace
   KD_TRY(scored_args(args, &a));
   KD_TRY(check_here({a.q, a.k, a.v, a.out, a.slopes, a.prefix, a.q_doc, a.kv_doc, a.kv_lengths, a.q_start}));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (args->dtype == KIMODO_FP32) {
-    KD_CUDA(attention_scored_f32(a, st));
-    return KIMODO_OK;
-  }
-  if (!gemm_tc_available()) return set_error(KIMODO_EUNSUPPORTED, "cuTensorMapEncodeTiled is unavailable");
+  const bool bf = args->dtype == KIMODO_BF16;
+  if (bf && !gemm_tc_available()) return set_error(KIMODO_EUNSUPPORTED, "cuTensorMapEncodeTiled is unavailable");
   const int sms = current_sms();
   if (sms < 1) return set_error(KIMODO_ECUDA, "the SM count could not be read");
-  const ScoredPlan plan = scored_attention_plan(a, sms);
+  const ScoredPlan plan = scored_attention_plan(a, bf, sms);
   if (plan.bytes > 0) {
     if (!workspace || workspace_bytes < plan.bytes)
       return set_error(KIMODO_EINVAL, "this call needs a workspace of %zu bytes (got %zu)", plan.bytes,
@@ -246,7 +244,7 @@ int kimodo_attention_scored(const kimodo_scored_attention* args, void* workspace
     if (misaligned(workspace, 16)) return set_error(KIMODO_EINVAL, "the workspace must be 16-byte aligned");
     KD_TRY(check_here({workspace}));
   }
-  KD_CUDA(attention_scored_bf16(a, plan, workspace, kernel_error_word(), st));
+  KD_CUDA(attention_scored(a, bf, plan, workspace, kernel_error_word(), st));
   return KIMODO_OK;
 }
 

@@ -174,14 +174,13 @@ struct ScoredAttention {
 // workspace of `bytes`, joined by a second kernel.
 struct ScoredPlan {
   int splits = 1, tiles_per_split = 1, row_blocks = 1, parts = 1;
-  bool alternate = false;
+  int few = 0;   // rows of the kernels for few rows (0: not those)
   float* part_o = nullptr;
   float* part_lse = nullptr;
   size_t bytes = 0;
 };
-ScoredPlan scored_attention_plan(const ScoredAttention& a, int num_sms);
-cudaError_t attention_scored_bf16(const ScoredAttention& a, ScoredPlan plan, void* workspace, DevError* err,
-                                  cudaStream_t st);
-cudaError_t attention_scored_f32(const ScoredAttention& a, cudaStream_t st);
+ScoredPlan scored_attention_plan(const ScoredAttention& a, bool is_bf16, int num_sms);
+cudaError_t attention_scored(const ScoredAttention& a, bool is_bf16, ScoredPlan plan, void* workspace, DevError* err,
+                             cudaStream_t st);
 
 }  // namespace kd

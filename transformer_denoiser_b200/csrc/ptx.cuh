@@ -364,6 +364,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// tmem_ld32 / tmem_ld16 into v[OFF] ... of a longer register array.
+template <int OFF, int N>
+__device__ __forceinline__ void tmem_ld32_at(uint32_t taddr, float (&v)[N]) {
+  static_assert(OFF + 32 <= N, "range");
+  float t[32];
+  tmem_ld32(taddr, t);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[OFF + i] = t[i];
+}
+template <int OFF, int N>
+__device__ __forceinline__ void tmem_ld16_at(uint32_t taddr, float (&v)[N]) {
+  static_assert(OFF + 16 <= N, "range");
+  float t[16];
+  tmem_ld16(taddr, t);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[OFF + i] = t[i];
+}
+
 // 4-D tiled load of one box into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
                                             int c3) {
