@@ -12,11 +12,12 @@
 // tokens fill one MMA tile together.
 //
 // Many rows (scored_tc_kernel): a CTA takes 256 rows as two 128-row tiles; while the softmax
-// of one runs, the tensor cores work on the other.  Roles (384 threads): warp 0 TMA of K and
-// V tiles (128 keys, 128-byte swizzle), warp 1 MMA issue, warps 4-7 and 8-11 softmax and
-// output of tile 0 and 1, one row a thread.  Per key tile and row tile: S = Q K^T into 128
-// TMEM columns; the row's thread reads S, forms p and writes it in bf16 over S; O += P V with
-// P as the TMEM operand.
+// of one runs, the tensor cores work on the other.  Roles (640 threads): warp 0 TMA of K and
+// V tiles (128 keys, 128-byte swizzle), warps 1 and 2 MMA issue of tile 0 and 1, warps 4-11 and 12-19 softmax and
+// output of tile 0 and 1, two threads a row, each half of the keys (one thread a row left the
+// four schedulers two warps each, too few to hide the latencies: 490 against 285 us for 16
+// heads x 8192 tokens).  Per key tile and row tile: S = Q K^T into 128 TMEM columns; the row's
+// threads read S, form p and write it in bf16 over S; O += P V with P as the TMEM operand.
 //
 // Few rows (scored_few_kernel, at most 64: new tokens over a cache): the keys take the MMA's
 // rows instead, S^T = K Q^T and O^T = V^T P^T, so that all four TMEM quarters, and with them
@@ -43,7 +44,7 @@ namespace kd {
 namespace {
 
 constexpr int TILE = 128;                    // query rows of a tile, keys of a tile
-constexpr int NUM_THREADS = 384;
+constexpr int NUM_THREADS = 640;
 constexpr int STAGES = 4;                    // K and V tiles in flight, alternating
 constexpr int MAX_FLAGS = 8192;              // key tiles whose document ranges a CTA keeps
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
@@ -58,38 +59,75 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // cap * tanh(x / cap) in log2 units.  For |x| <= cap: x * R((x / cap)^2) with R(u) = tanh(sqrt u) /
-// sqrt u by a polynomial of degree 6 (weighted least squares towards the relative minimax on
-// [0, 1]; relative error 5.0e-8), which costs no special-function slots: those are what bounds
+// sqrt u by a polynomial of degree 5 (weighted least squares towards the relative minimax on
+// [0, 1]; relative error 5.9e-7, on a cap of 50 at most 4e-5 of a weight, a hundredth of its
+// rounding to bf16), which costs no special-function slots: those are what bounds
 // the softmax.  Beyond (rare: the tile is then done again), tanh z = 1 - 2 / (1 + e^(2z)).
 struct CapCoef {
-  float z, lin;          // scale / cap; scale * log2 e
-  float limit;           // |s| up to which the polynomial holds
+  float z;               // scale / cap
+  float c[6];            // the polynomial times scale * log2 e
+  float limit;           // |s| up to which it holds
   float two, cap2;       // e^(2 s z) = 2^(two s); cap * log2 e
 };
 __device__ __forceinline__ CapCoef cap_coef(float scale, float cap) {
+  const float lin = scale * LOG2E;
   CapCoef k;
   k.z = scale / cap;
-  k.lin = scale * LOG2E;
+  k.c[0] = 0.9999994039535522f * lin;
+  k.c[1] = -0.3332904279232025f * lin;
+  k.c[2] = 0.13281433284282684f * lin;
+  k.c[3] = -0.051605645567178726f * lin;
+  k.c[4] = 0.01674308441579342f * lin;
+  k.c[5] = -0.003067048266530037f * lin;
   k.limit = 1.f / fabsf(k.z);
   k.two = 2.f * LOG2E * k.z;
   k.cap2 = cap * LOG2E;
   return k;
 }
-// two scores at once (f32x2 arithmetic)
-__device__ __forceinline__ float2 capped_poly(const CapCoef& k, float2 s) {
+// s * ratio = cap * tanh(scale s / cap) in log2 units, two scores at once (f32x2 arithmetic)
+__device__ __forceinline__ float2 cap_ratio(const CapCoef& k, float2 s) {
   const float2 z = __fmul2_rn(s, make_float2(k.z, k.z));
   const float2 u = __fmul2_rn(z, z);
-  auto step = [&](float2 r, float c) { return __ffma2_rn(r, u, make_float2(c, c)); };
-  float2 r = step(make_float2(0.0010410185204818845f, 0.0010410185204818845f), -0.006203366909176111f);
-  r = step(r, 0.020289966836571693f);
-  r = step(r, -0.053457021713256836f);
-  r = step(r, 0.13325203955173492f);
-  r = step(r, -0.33332839608192444f);
-  r = step(r, 0.9999999403953552f);
-  return __fmul2_rn(__fmul2_rn(s, make_float2(k.lin, k.lin)), r);
+  float2 r = make_float2(k.c[5], k.c[5]);
+#pragma unroll
+  for (int i = 4; i >= 0; --i) r = __ffma2_rn(r, u, make_float2(k.c[i], k.c[i]));
+  return r;
 }
+__device__ __forceinline__ float2 capped_poly(const CapCoef& k, float2 s) { return __fmul2_rn(s, cap_ratio(k, s)); }
 __device__ __forceinline__ float capped_any(const CapCoef& k, float s) {
   return fmaf(-2.f * k.cap2, rcp_approx(1.f + ex2(s * k.two)), k.cap2);
+}
+
+// 3-operand maximum and minimum (a NaN operand is passed over, as by fmaxf)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ float max_of(const float (&x)[N]) {
+  float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
+#pragma unroll
+  for (int e = 4; e < N; e += 4) {
+    a = max3(a, x[e], x[e + 1]);
+    b = max3(b, x[e + 2], x[e + 3]);
+  }
+  return fmaxf(a, b);
+}
+template <int N>
+__device__ __forceinline__ float min_of(const float (&x)[N]) {
+  float a = fminf(x[0], x[1]), b = fminf(x[2], x[3]);
+#pragma unroll
+  for (int e = 4; e < N; e += 4) {
+    a = min3(a, x[e], x[e + 1]);
+    b = min3(b, x[e + 2], x[e + 3]);
+  }
+  return fminf(a, b);
 }
 
 __device__ __forceinline__ void record_timeout(DevError* err, volatile int* abort) {
@@ -180,7 +218,7 @@ struct Cfg {
   static constexpr uint32_t HALF = TILE * 128;             // 64 dims of a tile
   // HD 64 would let two CTAs share an SM, whose TMEM holds one: the size keeps them apart
   static constexpr size_t BODY = 2 * Q_BYTES + (size_t)STAGES * KV_BYTES;
-  static constexpr size_t SMEM = 1024 + (BODY < 119808 ? 119808 : BODY) + MAX_FLAGS + 256 + 8 * TILE * 4;
+  static constexpr size_t SMEM = 1024 + (BODY < 119808 ? 119808 : BODY) + MAX_FLAGS + 256 + 16 * 64 * 4 + 2 * 2 * 2 * TILE * 4;
 };
 constexpr uint32_t TMEM_COLS = 512;
 __device__ __forceinline__ uint32_t s_col(int t) { return 128u * t; }
@@ -205,7 +243,7 @@ struct RowTile {
 };
 
 template <int HD, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(NUM_THREADS, 1)   // 168 registers a thread
+__global__ void __launch_bounds__(NUM_THREADS, 1)   // 96 registers a thread
 scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ ScoredAttention a, const ScoredPlan plan, DevError* err) {
   using C = Cfg<HD>;
@@ -221,11 +259,11 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   auto s_bar = [&](int t) { return bar0 + 8u * (2 * STAGES + t); };       // S formed
   auto p_bar = [&](int t) { return bar0 + 8u * (2 * STAGES + 2 + t); };   // P written, O rescaled
   auto o_bar = [&](int t) { return bar0 + 8u * (2 * STAGES + 4 + t); };   // last P V done
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 6);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 7);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 6);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   RowTile* tiles = reinterpret_cast<RowTile*>(tmem_slot + 2);
-  int* docs_smem = reinterpret_cast<int*>(smem + C::BODY + MAX_FLAGS + 256);   // [8 warps][TILE]
+  int* docs_smem = reinterpret_cast<int*>(smem + C::BODY + MAX_FLAGS + 256);   // [16 warps][64]
+  float* xch = reinterpret_cast<float*>(docs_smem + 16 * 64);                  // [2 turns][2 tiles][2 halves][TILE]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // block = ((row block, last first) * Hkv * B + (b * Hkv + hk)) * splits + split
@@ -242,17 +280,16 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       ptx::mbar_init(full_bar(s), 1);
-      ptx::mbar_init(empty_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 2);
     }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(s_bar(t), 1);
-      ptx::mbar_init(p_bar(t), 4);
+      ptx::mbar_init(p_bar(t), 8);
       ptx::mbar_init(o_bar(t), 1);
       tiles[t].docs_lo = INT_MAX;
       tiles[t].docs_hi = -1;
       tiles[t].any_none = 0;
     }
-    ptx::mbar_init(drain_bar, 1);
     ptx::fence_mbar_init();
     *abort = 0;
     ptx::tma_prefetch_desc(&tmK);
@@ -286,7 +323,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     ptx::fence_proxy_async_smem();
   }
   // this softmax thread's row
-  const int t_own = warp >= 8 ? 1 : 0;
+  const int t_own = warp >= 12 ? 1 : 0;
   const int lr_own = (warp & 3) * 32 + lane + t_own * TILE;
   const int r_own = row0 + lr_own;
   const bool row_ok = warp >= 4 && r_own < rows;
@@ -356,264 +393,256 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  // all columns are this CTA's, so they start at 0 (a constant the MMA operands are made of)
+  constexpr uint32_t tmem_base = 0;
 
-  // Which of the row tiles take key tile jt (bits 0 and 1).
-  int last_pos[2];
-  bool alive[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int r_a = row0 + t * TILE;
-    const int r_b = min(r_a + TILE, rows) - 1;
-    alive[t] = r_a < rows;
-    last_pos[t] = seq.start + max(r_b, 0) / a.G;
-  }
-  auto needed = [&](int jt) -> int {
-    const int j0 = jt * TILE;
-    int need = 0;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      bool n = alive[t] && (!a.causal || j0 <= last_pos[t] || j0 < seq.prefix);
-      if (listed) n = n && ((flags[jt - jt0] >> (2 * t)) & 1);
-      need |= n ? 1 << t : 0;
-    }
-    return need;
+  // Row tile t takes the key tiles [jt0, end_t) that hold a document of its rows.
+  auto end_of = [&](int t) {
+    const int r_a = row0 + t * TILE, r_b = min(r_a + TILE, rows) - 1;
+    if (r_a >= rows) return 0;
+    return min((1 + last_key(a, seq, (long)seq.start + r_b / a.G) + TILE - 1) / TILE, jt1);
+  };
+  const int end0 = end_of(0), end1 = end_of(1);
+  auto takes = [&](int t, int jt) -> bool {
+    return jt < (t ? end1 : end0) && (!listed || ((flags[jt - jt0] >> (2 * t)) & 1));
   };
 
-  // registers: 384 x 168 at launch cover 128 x 80 + 256 x 208
+  // registers: 640 x 96 at launch cover 128 x 64 + 512 x 104
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA: K and V tile of every key tile taken, in turn
-      int stage = 0;
-      uint32_t phase = 0;
-      long issued = 0;
-      bool ok = true;
-      for (int jt = jt0; jt < jt1 && ok; ++jt) {
-        if (!needed(jt)) continue;
-        for (int kv = 0; kv < 2; ++kv) {
-          if (!ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort, WAIT_LIMIT_NS)) {
-            ok = false;
-            break;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0) {
+      if (lane == 0) {
+        // ---------------- TMA: K and V tile of every key tile that a row tile takes
+        int stage = 0;
+        uint32_t phase = 0;
+        long issued = 0;
+        bool ok = true;
+        for (int jt = jt0; jt < jt1 && ok; ++jt) {
+          if (!takes(0, jt) && !takes(1, jt)) continue;
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort, WAIT_LIMIT_NS)) {
+              ok = false;
+              break;
+            }
+            ptx::mbar_arrive_expect_tx(full_bar(stage), C::KV_BYTES);
+#pragma unroll
+            for (int hf = 0; hf < HD / 64; ++hf)
+              ptx::tma_load_4d(sKV + stage * C::KV_BYTES + hf * C::HALF, kv ? &tmV : &tmK, full_bar(stage), hf * 64,
+                               jt * TILE, hk, b);
+            ++issued;
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
-          ptx::mbar_arrive_expect_tx(full_bar(stage), C::KV_BYTES);
-#pragma unroll
-          for (int hf = 0; hf < HD / 64; ++hf)
-            ptx::tma_load_4d(sKV + stage * C::KV_BYTES + hf * C::HALF, kv ? &tmV : &tmK, full_bar(stage), hf * 64,
-                             jt * TILE, hk, b);
-          ++issued;
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok && !*abort) record_timeout(err, abort);
+        // every copy issued has landed before the CTA leaves (also after a wait that ran out)
+        const long n = issued < STAGES ? issued : STAGES;
+        volatile int never = 0;
+        for (long i = 0; i < n; ++i) {
+          if (--stage < 0) { stage = STAGES - 1; phase ^= 1u; }
+          ptx::mbar_wait_bounded(full_bar(stage), phase, &never, WAIT_LIMIT_NS);
         }
       }
-      if (!ok && !*abort) record_timeout(err, abort);
-      // every copy issued has landed before the CTA leaves (also after a wait that ran out)
-      const long n = issued < STAGES ? issued : STAGES;
-      volatile int never = 0;
-      for (long i = 0; i < n; ++i) {
-        if (--stage < 0) { stage = STAGES - 1; phase ^= 1u; }
-        ptx::mbar_wait_bounded(full_bar(stage), phase, &never, WAIT_LIMIT_NS);
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------- MMA: per key tile and row tile t, first P V of the tile before, then Q K^T
-    // (which overwrites that P); the other row tile's products run while t's softmax does
-    const uint32_t idesc_s = ptx::idesc_bf16_f32(TILE, TILE);
-    const uint32_t idesc_o = ptx::idesc_bf16_f32(TILE, HD) | (1u << 16);
-    int stage = 0, pend = 0, v_stage = 0, v_rows = TILE;
-    uint32_t phase = 0, v_phase = 0, p_phase[2] = {0, 0};
-    bool started[2] = {false, false}, ok = true;
-    auto advance = [&](int& s, uint32_t& ph) { if (++s == STAGES) { s = 0; ph ^= 1u; } };
-    auto pv = [&](int t) -> bool {   // O_t (+)= P_t V of the pending value tile
-      if (!ptx::mbar_wait_bounded(p_bar(t), p_phase[t], abort, WAIT_LIMIT_NS)) return false;
-      p_phase[t] ^= 1u;
-      ptx::tc_fence_after();
-      if (lane == 0) {
-        const uint32_t v = sKV + v_stage * C::KV_BYTES;
-#pragma unroll
-        for (int kk = 0; kk < TILE / 16; ++kk)
-          ptx::tc_mma_bf16_ta(tmem_base + o_col<HD>(t), tmem_base + s_col(t) + kk * 8, desc_mn(v + kk * 2048, C::HALF),
-                              idesc_o, started[t] || kk != 0);
-      }
-      started[t] = true;
-      __syncwarp();
-      return true;
-    };
-    auto values_ready = [&]() -> bool {
-      if (!ptx::mbar_wait_bounded(full_bar(v_stage), v_phase, abort, WAIT_LIMIT_NS)) return false;
-      if (v_rows < TILE) {   // value rows past the last key: 0, whatever they hold
-        uint8_t* v = smem + 2 * C::Q_BYTES + v_stage * C::KV_BYTES;
-        const int n = (TILE - v_rows) * 8;
-        for (int c = lane; c < n * (HD / 64); c += 32) {
-          const int hf = c / n, e = c % n;
-          *reinterpret_cast<uint4*>(v + hf * C::HALF + (v_rows + e / 8) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-      }
-      return true;
-    };
-    for (int jt = jt0; jt <= jt1 && ok; ++jt) {
-      const bool end = jt == jt1;
-      const int need = end ? 0 : needed(jt);
-      if (!end && !need) continue;
-      int k_stage = stage;
-      if (!end) {
-        ok = ptx::mbar_wait_bounded(full_bar(stage), phase, abort, WAIT_LIMIT_NS);
-        if (!ok) break;
-        advance(stage, phase);
-      }
-      ptx::tc_fence_after();
-      auto qk = [&](int t) {
-        if (lane == 0) {
-          const uint32_t q = sQ + t * C::Q_BYTES, k = sKV + k_stage * C::KV_BYTES;
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            ptx::tc_mma_bf16(tmem_base + s_col(t), ptx::smem_desc_sw128(q + (kk >> 2) * C::HALF + (kk & 3) * 32),
-                             ptx::smem_desc_sw128(k + (kk >> 2) * C::HALF + (kk & 3) * 32), idesc_s, kk != 0);
-          ptx::tc_commit(s_bar(t));
-        }
-        __syncwarp();
+    } else if (warp < 3) {
+      // ---------------- MMA of row tile t: per key tile first P V of the tile before, then Q K^T,
+      // which overwrites that P.  The tiles' MMAs come from two warps, so that neither waits
+      // for the other's softmax, and from two schedulers: their issue slots are scarce beside
+      // the softmax warps.  Control flow and operands are uniform over the warp.
+      const int t = warp - 1;
+      const uint32_t idesc_s = ptx::idesc_bf16_f32(TILE, TILE);
+      const uint32_t idesc_o = ptx::idesc_bf16_f32(TILE, HD) | (1u << 16);
+      // operand descriptors: low words of the first stage, later ones and K steps by additions
+      const uint64_t d_k = ptx::smem_desc_sw128(sKV), d_v = desc_mn(sKV, C::HALF);
+      const uint32_t k_hi = (uint32_t)(d_k >> 32), v_hi = (uint32_t)(d_v >> 32);
+      const uint32_t q_lo = (uint32_t)ptx::smem_desc_sw128(sQ + t * C::Q_BYTES);
+      const uint32_t s_tmem = tmem_base + s_col(t), o_tmem = tmem_base + o_col<HD>(t);
+      int stage = 0, v_stage = 0, v_rows = TILE;
+      uint32_t phase = 0, v_phase = 0, p_phase = 0, started = 0;
+      bool ok = true, pend = false;
+      auto wait = [&](uint32_t bar, uint32_t ph) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, ph, abort, WAIT_LIMIT_NS));
+        return ok;
       };
-      // scores of a row tile with no weights outstanding first: they wait for nothing
+      auto pv = [&]() {   // O (+)= P V of the pending key tile
+        if (!wait(full_bar(v_stage), v_phase)) return;
+        if (v_rows < TILE) {   // value rows past the last key: 0, whatever they hold
+          uint8_t* v = smem + 2 * C::Q_BYTES + v_stage * C::KV_BYTES;
+          const int n = (TILE - v_rows) * 8;
+          for (int c = lane; c < n * (HD / 64); c += 32) {
+            const int hf = c / n, e = c % n;
+            *reinterpret_cast<uint4*>(v + hf * C::HALF + (v_rows + e / 8) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!wait(p_bar(t), p_phase)) return;
+        p_phase ^= 1u;
+        ptx::tc_fence_after();
+        const uint32_t v_lo = (uint32_t)d_v + v_stage * (C::KV_BYTES >> 4);
+        if (ptx::elect_one()) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if ((need & ~pend) >> t & 1) qk(t);
-      if (pend) ok = values_ready();
+          for (int kk = 0; kk < TILE / 16; ++kk)
+            ptx::tc_mma_bf16_ta_lo(o_tmem, s_tmem + kk * 8, v_lo + kk * (2048 >> 4), v_hi, idesc_o,
+                                   kk != 0 ? 1u : started);
+          ptx::tc_commit(empty_bar(v_stage));
+        }
+        __syncwarp();
+        started = 1u;
+        pend = false;
+      };
+      for (int jt = jt0; jt < jt1; ++jt) {
+        const bool mine = __shfl_sync(0xffffffffu, (int)takes(t, jt), 0) != 0;
+        const bool other = __shfl_sync(0xffffffffu, (int)takes(t ^ 1, jt), 0) != 0;
+        if (!mine && !other) continue;
+        const int k_stage = stage;
+        const uint32_t k_phase = phase;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        if (mine && !wait(full_bar(k_stage), k_phase)) break;
+        if (pend) {
+          pv();
+          if (!ok) break;
+        }
+        if (mine) {
+          ptx::tc_fence_after();
+          const uint32_t k_lo = (uint32_t)d_k + k_stage * (C::KV_BYTES >> 4);
+          if (ptx::elect_one()) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (ok && (pend >> t & 1)) ok = pv(t);
-        if (ok && ((need & pend) >> t & 1)) qk(t);
+            for (int kk = 0; kk < HD / 16; ++kk)
+              ptx::tc_mma_bf16_lo(s_tmem, q_lo + (((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4),
+                                  k_lo + (((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4), k_hi, idesc_s, kk != 0);
+            ptx::tc_commit(s_bar(t));
+            ptx::tc_commit(empty_bar(k_stage));
+          }
+          __syncwarp();
+          pend = true;
+          v_stage = stage;
+          v_phase = phase;
+          v_rows = min(seq.kv_len - jt * TILE, TILE);
+        } else {   // the other tile's alone: hand both stages on, once they have been filled
+          if (!wait(full_bar(k_stage), k_phase) || !wait(full_bar(stage), phase)) break;
+          if (lane == 0) {
+            ptx::mbar_arrive(empty_bar(k_stage));
+            ptx::mbar_arrive(empty_bar(stage));
+          }
+        }
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      if (!ok) break;
-      if (lane == 0) {
-        if (!end) ptx::tc_commit(empty_bar(k_stage));
-        if (pend) ptx::tc_commit(empty_bar(v_stage));
+      if (ok && pend) pv();
+      if (!ok && !*abort && lane == 0) record_timeout(err, abort);
+      if (ptx::elect_one()) {
+        ptx::tc_commit(o_bar(t));
+        volatile int never = 0;
+        if (!ptx::mbar_wait_bounded(o_bar(t), 0, &never, WAIT_LIMIT_NS)) record_timeout(err, abort);
       }
       __syncwarp();
-      if (!end) {
-        pend = need;
-        v_stage = stage;
-        v_phase = phase;
-        v_rows = min(seq.kv_len - jt * TILE, TILE);
-        advance(stage, phase);
-      }
     }
-    if (!ok && !*abort && lane == 0) record_timeout(err, abort);
-    if (lane == 0) {
-      ptx::tc_commit(o_bar(0));
-      ptx::tc_commit(o_bar(1));
-      ptx::tc_commit(drain_bar);
-      volatile int never = 0;
-      if (!ptx::mbar_wait_bounded(drain_bar, 0, &never, WAIT_LIMIT_NS)) record_timeout(err, abort);
-    }
-    __syncwarp();
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---------------- softmax and output of row tile t_own
     const int t = t_own;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem_base + lane_addr + s_col(t), o_addr = tmem_base + lane_addr + o_col<HD>(t);
+    const int half = ((warp - 4) >> 2) & 1;            // keys 64 half .. of a tile, dims likewise
+    constexpr int KH = TILE / 2, DH2 = HD / 2;
+    const int lrow = (warp & 3) * 32 + lane;
+    const int pair_bar = 1 + t * 4 + (warp & 3);       // the two warps that share 32 rows
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
     const bool warp_rows = (warp & 3) * 32 + row0 + t * TILE < rows;
     const int p = seq.start + i_own;
     const int last = row_ok ? last_key(a, seq, (long)seq.start + i_own) : -1;
     const float slope2 = BIAS && row_ok ? a.slopes[hk * a.G + g_own] * LOG2E : 0.f;
-    const CapCoef cc = cap_coef(a.scale, CAP ? a.cap : 1.f);
+    // Scores grow with the raw product (after its sign is that of the scale) where there is no
+    // bias; a scale of 0 is a product of 0.
+    const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
+    const CapCoef cc = cap_coef(scale, CAP ? a.cap : 1.f);
     // Without cap and bias the scale is applied with the reference's subtraction (one FMA), so
-    // the maximum is taken of the raw scores, signed so that the factor is positive.
+    // the maximum is taken of the raw scores.
     constexpr bool RAW = !CAP && !BIAS;
-    const float sc = a.scale * LOG2E;
-    const float mul = RAW ? (sc == 0.f ? 1.f : fabsf(sc)) : 1.f;
+    const float sc = scale * LOG2E;
     const int* kdocs = docs ? a.kv_doc + (long)b * a.Sk : nullptr;
-    int* dbuf = docs_smem + (warp - 4) * TILE;
+    int* dbuf = docs_smem + (warp - 4) * KH;
     float m = -INFINITY;            // reference of the weights (log2 units)
-    float2 l2 = make_float2(0.f, 0.f);   // their sum
+    float2 l2 = make_float2(0.f, 0.f);   // their sum over this thread's keys
     uint32_t phase = 0;
     bool ok = true, started = false;
-    for (int jt = jt0; jt < jt1; ++jt) {
-      if (!(needed(jt) >> t & 1)) continue;
-      const int j0 = jt * TILE;
+    const int end_t = t ? end1 : end0;
+    for (int jt = jt0; jt < end_t; ++jt) {
+      if (listed && !((flags[jt - jt0] >> (2 * t)) & 1)) continue;
+      const int j0 = jt * TILE + half * KH;
       const bool one_doc = !docs || (listed && ((flags[jt - jt0] >> (2 * t + 1)) & 1));
-      if (!one_doc) {   // the tile's documents, staged before the scores are there
-#pragma unroll
-        for (int e = 0; e < TILE / 32; ++e) dbuf[e * 32 + lane] = kdocs[min(j0 + e * 32 + lane, a.Sk - 1)];
+      if (!one_doc) {   // the documents of these keys, staged before the scores are there
+        dbuf[lane] = kdocs[min(j0 + lane, a.Sk - 1)];
+        dbuf[32 + lane] = kdocs[min(j0 + 32 + lane, a.Sk - 1)];
         __syncwarp();
       }
-      ok = ptx::mbar_wait_bounded(s_bar(t), phase, abort, WAIT_LIMIT_NS);
-      if (!ok) break;
-      phase ^= 1u;
+      // after a wait that ran out the rest is gone through without waiting, so that the
+      // barriers of the warp pairs stay matched
+      if (ok) ok = ptx::mbar_wait_bounded(s_bar(t), phase, abort, WAIT_LIMIT_NS);
       if (warp_rows) {
         ptx::tc_fence_after();
-        // scores (RAW: before their scale; else in log2 units), masked ones -infinity
-        float x[TILE];
-        ptx::tmem_ld32_at<0>(s_addr, x);
-        ptx::tmem_ld32_at<32>(s_addr + 32, x);
-        ptx::tmem_ld32_at<64>(s_addr + 64, x);
-        ptx::tmem_ld32_at<96>(s_addr + 96, x);
+        float x[KH];
+        ptx::tmem_ld32_at<0>(s_addr + half * KH, x);
+        ptx::tmem_ld32_at<32>(s_addr + half * KH + 32, x);
         ptx::tmem_ld_wait();
+        if (a.scale <= 0.f) {
+#pragma unroll
+          for (int e = 0; e < KH; ++e) x[e] = a.scale < 0.f ? -x[e] : 0.f;
+        }
+        const bool masked = !one_doc || !__all_sync(0xffffffffu, j0 + KH - 1 <= last || !row_ok);
+        float top = RAW ? 0.f : max_of(x);
+        bool direct = false;   // CAP alone: x stays raw, the cap is applied with the reference
         if constexpr (CAP) {
-          float far = fabsf(x[0]);
+          const bool near = !__any_sync(0xffffffffu, !(fmaxf(top, -min_of(x)) <= cc.limit));
+          direct = !BIAS && near && !masked;
+          if (direct) {
+            top = capped_poly(cc, make_float2(top, top)).x;
+          } else if (near) {
 #pragma unroll
-          for (int e = 1; e < TILE; ++e) far = fmaxf(far, fabsf(x[e]));
-          if (__any_sync(0xffffffffu, !(far <= cc.limit))) {
-#pragma unroll
-            for (int e = 0; e < TILE; ++e) x[e] = capped_any(cc, x[e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < TILE; e += 2) {
+            for (int e = 0; e < KH; e += 2) {
               const float2 y = capped_poly(cc, make_float2(x[e], x[e + 1]));
               x[e] = y.x;
               x[e + 1] = y.y;
             }
-          }
-        } else if constexpr (RAW) {
-          if (sc <= 0.f) {
+          } else {
 #pragma unroll
-            for (int e = 0; e < TILE; ++e) x[e] = sc < 0.f ? -x[e] : 0.f;
+            for (int e = 0; e < KH; ++e) x[e] = capped_any(cc, x[e]);
           }
         }
         if constexpr (BIAS) {
           const float d0 = (float)(p - j0);
 #pragma unroll
-          for (int e = 0; e < TILE; ++e)
-            x[e] = fmaf(-slope2, fabsf(d0 - (float)e), CAP ? x[e] : x[e] * sc);
+          for (int e = 0; e < KH; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), CAP ? x[e] : x[e] * sc);
         }
-        if (!__all_sync(0xffffffffu, j0 + TILE - 1 <= last || !row_ok)) {
+        if (masked) {
 #pragma unroll
-          for (int e = 0; e < TILE; ++e)
+          for (int e = 0; e < KH; ++e)
             if (j0 + e > last) x[e] = -INFINITY;
-        }
-        if (!one_doc) {
+          if (!one_doc) {
 #pragma unroll
-          for (int e = 0; e < TILE; e += 4) {
-            const int4 d = *reinterpret_cast<const int4*>(dbuf + e);
-            if (d.x != qdoc) x[e] = -INFINITY;
-            if (d.y != qdoc) x[e + 1] = -INFINITY;
-            if (d.z != qdoc) x[e + 2] = -INFINITY;
-            if (d.w != qdoc) x[e + 3] = -INFINITY;
-          }
-          if (qdoc < 0) {
-#pragma unroll
-            for (int e = 0; e < TILE; ++e) x[e] = -INFINITY;
+            for (int e = 0; e < KH; e += 4) {
+              const int4 d = *reinterpret_cast<const int4*>(dbuf + e);
+              if (d.x != qdoc || qdoc < 0) x[e] = -INFINITY;
+              if (d.y != qdoc || qdoc < 0) x[e + 1] = -INFINITY;
+              if (d.z != qdoc || qdoc < 0) x[e + 2] = -INFINITY;
+              if (d.w != qdoc || qdoc < 0) x[e + 3] = -INFINITY;
+            }
           }
         }
-        float t0 = fmaxf(x[0], x[1]), t1 = fmaxf(x[2], x[3]);
-#pragma unroll
-        for (int e = 4; e < TILE; e += 4) {
-          t0 = fmaxf(fmaxf(t0, x[e]), x[e + 1]);
-          t1 = fmaxf(fmaxf(t1, x[e + 2]), x[e + 3]);
-        }
-        const float top = fmaxf(t0, t1) * mul;
+        if (!direct) top = max_of(x);
+        if (RAW) top *= sc;
+        // the other half's maximum
+        float* xm = xch + ((phase * 2 + t) * 2) * TILE;
+        xm[half * TILE + lrow] = top;
+        pair_sync();
+        top = fmaxf(top, xm[(half ^ 1) * TILE + lrow]);
         // move the reference: at once while there is none, later only when it falls far behind
         const bool move = !started || top > m + RESCALE_AT;
         const float m_new = move ? fmaxf(m, top) : m;
-        if (started && __any_sync(0xffffffffu, move)) {
+        if (started && __any_sync(0xffffffffu, move)) {   // both warps of the rows alike
           const float f = m_new == m ? 1.f : ex2(m - m_new);   // m = -infinity: 0
           l2.x *= f;
           l2.y *= f;
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 16) {
+          for (int c = half * DH2; c < (half + 1) * DH2; c += 16) {
             float v[16];
             uint32_t w[16];
             ptx::tmem_ld(o_addr + c, v);
@@ -625,39 +654,56 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         m = m_new;
         const float ref = m == -INFINITY ? 0.f : m;
-        const float2 mul2 = make_float2(mul, mul), nref2 = make_float2(-ref, -ref);
+        const float2 nref2 = make_float2(-ref, -ref), sc2 = make_float2(sc, sc);
+        // weights over the scores: this half's 64 in 32 columns (the other half has read its own)
+        auto weights = [&](auto arg) {
 #pragma unroll
-        for (int c = 0; c < TILE; c += 32) {
-          uint32_t w[16];
+          for (int c = 0; c < KH; c += 32) {
+            uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 xv = make_float2(x[c + e], x[c + e + 1]);
-            const float2 y = RAW ? __ffma2_rn(xv, mul2, nref2) : __fadd2_rn(xv, nref2);
-            const float2 pw = make_float2(ex2(y.x), ex2(y.y));
-            l2 = __fadd2_rn(l2, pw);
-            w[e / 2] = bf16x2_bits(pw.x, pw.y);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 y = arg(make_float2(x[c + e], x[c + e + 1]));
+              const float2 pw = make_float2(ex2(y.x), ex2(y.y));
+              l2 = __fadd2_rn(l2, pw);
+              w[e / 2] = bf16x2_bits(pw.x, pw.y);
+            }
+            ptx::tmem_st16(s_addr + half * (KH / 2) + c / 2, w);
           }
-          ptx::tmem_st16(s_addr + c / 2, w);
+        };
+        if (RAW) {
+          weights([&](float2 v) { return __ffma2_rn(v, sc2, nref2); });
+        } else if (CAP && !BIAS) {
+          if (direct)
+            weights([&](float2 v) { return __ffma2_rn(v, cap_ratio(cc, v), nref2); });
+          else
+            weights([&](float2 v) { return __fadd2_rn(v, nref2); });
+        } else {
+          weights([&](float2 v) { return __fadd2_rn(v, nref2); });
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
       }
+      phase ^= 1u;
       started = true;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(p_bar(t));
     }
-    const float l = l2.x + l2.y;
     if (ok) ok = ptx::mbar_wait_bounded(o_bar(t), 0, abort, WAIT_LIMIT_NS);
     if (!ok && !*abort) record_timeout(err, abort);
-    if (ok && warp_rows) {
+    if (warp_rows) {   // also after a wait that ran out: the pair's barriers stay matched
+      float* xs = xch + t * 2 * TILE;
+      pair_sync();     // the maxima have been read
+      xs[half * TILE + lrow] = l2.x + l2.y;
+      pair_sync();
+      const float l = xs[lrow] + xs[TILE + lrow];
       ptx::tc_fence_after();
       const bool seen = started && l != 0.f;   // l is NaN where a score is
       const float inv = seen ? 1.f / l : 0.f;
-      bool finite = true;
-      if (plan.parts == 1) {
+      if (ok && plan.parts == 1) {
+        bool finite = true;
         bf16* o = static_cast<bf16*>(a.out) + b * a.o_batch + i_own * a.o_token + (long)(hk * a.G + g_own) * a.o_head;
 #pragma unroll 1
-        for (int c = 0; c < HD; c += 16) {
+        for (int c = half * DH2; c < (half + 1) * DH2; c += 16) {
           float v[16];
           ptx::tmem_ld(o_addr + c, v);
           ptx::tmem_ld_wait();
@@ -673,31 +719,31 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             *reinterpret_cast<uint4*>(o + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
-        unsigned redo = __ballot_sync(0xffffffffu, row_ok && !finite);
+        pair_sync();   // the sums have been read; both halves are written
+        xs[half * TILE + lrow] = finite ? 0.f : 1.f;
+        pair_sync();
+        unsigned redo = half == 0 ? __ballot_sync(0xffffffffu, row_ok && xs[lrow] + xs[TILE + lrow] != 0.f) : 0u;
         while (redo) {
           const int src = __ffs(redo) - 1;
           redo &= redo - 1;
           row_by_warp<bf16, HD>(a, b, hk * a.G + __shfl_sync(0xffffffffu, g_own, src),
                                 __shfl_sync(0xffffffffu, i_own, src));
         }
-      } else {
+      } else if (ok) {
         // a part: the result over these keys and the log2 of its weight
-        const int part = split;
         const long prow = ((long)b * a.Hkv + hk) * rows + r_own;
         const long n_rows = (long)a.B * a.Hkv * rows;
-        float* o = plan.part_o + ((long)part * n_rows + prow) * HD;
-        if (row_ok) plan.part_lse[(long)part * n_rows + prow] = seen ? m + log2f(l) : -INFINITY;
+        float* o = plan.part_o + ((long)split * n_rows + prow) * HD;
+        if (row_ok && half == 0) plan.part_lse[(long)split * n_rows + prow] = seen ? m + log2f(l) : -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < HD; c += 16) {
+        for (int c = half * DH2; c < (half + 1) * DH2; c += 16) {
           float v[16];
           ptx::tmem_ld(o_addr + c, v);
           ptx::tmem_ld_wait();
-          if (row_ok) {
+          if (row_ok && seen) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(o + c + e) =
-                  seen ? make_float4(v[e] * inv, v[e + 1] * inv, v[e + 2] * inv, v[e + 3] * inv)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+              *reinterpret_cast<float4*>(o + c + e) = make_float4(v[e] * inv, v[e + 1] * inv, v[e + 2] * inv, v[e + 3] * inv);
           }
         }
       }
@@ -707,7 +753,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, TMEM_COLS);
+    ptx::tmem_dealloc(*tmem_slot, TMEM_COLS);
   }
 }
 
@@ -863,6 +909,8 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const uint32_t idesc_o = ptx::idesc_bf16_f32(TILE, NR) | (1u << 15);
     // 64 dims: both 64-row halves of the MMA read the same values, the second half is not used
     constexpr uint32_t V_ATOM = HD == 128 ? C::HALF : 0u;
+    const uint64_t q_desc = ptx::smem_desc_sw128(sQ), p_desc = ptx::smem_desc_sw128(sP);
+    const uint64_t k_desc0 = ptx::smem_desc_sw128(sKV), v_desc0 = desc_mn(sKV, V_ATOM);
     bool ok = true;
     auto stage_of = [](int i) { return i % NST; };
     auto phase_of = [](int i) { return (uint32_t)((i / NST) & 1); };
@@ -870,12 +918,12 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       ok = ptx::mbar_wait_bounded(full_bar(stage_of(2 * n)), phase_of(2 * n), abort, WAIT_LIMIT_NS);
       if (!ok) return;
       ptx::tc_fence_after();
-      if (lane == 0) {
-        const uint32_t k = sKV + stage_of(2 * n) * C::KV_BYTES;
+      const uint64_t k = k_desc0 + (uint64_t)(stage_of(2 * n) * (C::KV_BYTES >> 4));
+      if (ptx::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          ptx::tc_mma_bf16(tmem_base + (n & 1) * NR, ptx::smem_desc_sw128(k + (kk >> 2) * C::HALF + (kk & 3) * 32),
-                           ptx::smem_desc_sw128(sQ + (kk >> 2) * (NR * 128) + (kk & 3) * 32), idesc_s, kk != 0);
+          ptx::tc_mma_bf16(tmem_base + (n & 1) * NR, k + (uint64_t)(((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4),
+                           q_desc + (uint64_t)(((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4), idesc_s, kk != 0);
         ptx::tc_commit(empty_bar(stage_of(2 * n)));
         ptx::tc_commit(s_bar(n & 1));
       }
@@ -901,19 +949,21 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       ok = ptx::mbar_wait_bounded(p_bar, n & 1, abort, WAIT_LIMIT_NS);
       if (!ok) break;
       ptx::tc_fence_after();
-      if (lane == 0) {
-        const uint32_t v = sKV + vs * C::KV_BYTES;
+      const uint64_t v = v_desc0 + (uint64_t)(vs * (C::KV_BYTES >> 4));
+      const uint32_t more = n != 0 ? 1u : 0u;
+      if (ptx::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < TILE / 16; ++kk)
-          ptx::tc_mma_bf16(tmem_base + 2 * NR, desc_mn(v + kk * 2048, V_ATOM),
-                           ptx::smem_desc_sw128(sP + (kk >> 2) * (NR * 128) + (kk & 3) * 32), idesc_o, (n | kk) != 0);
+          ptx::tc_mma_bf16(tmem_base + 2 * NR, v + (uint64_t)(kk * (2048 >> 4)),
+                           p_desc + (uint64_t)(((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4), idesc_o,
+                           kk != 0 ? 1u : more);
         ptx::tc_commit(empty_bar(vs));
         ptx::tc_commit(o_bar);
       }
       __syncwarp();
     }
     if (!ok && !*abort && lane == 0) record_timeout(err, abort);
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       ptx::tc_commit(drain_bar);
       volatile int never = 0;
       if (!ptx::mbar_wait_bounded(drain_bar, 0, &never, WAIT_LIMIT_NS)) record_timeout(err, abort);
@@ -940,8 +990,9 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     for (int n = 0; n < n_tiles; ++n) {
       const int j = (jt0 + n) * TILE + key;
       const int kd = docs ? a.kv_doc[(long)b * a.Sk + min(j, a.Sk - 1)] : 0;
-      ok = ptx::mbar_wait_bounded(s_bar(n & 1), (n >> 1) & 1, abort, WAIT_LIMIT_NS);
-      if (!ok) break;
+      // (after a wait that ran out the rest is gone through without waiting, so that the
+      // barriers of the four warps stay matched)
+      if (ok) ok = ptx::mbar_wait_bounded(s_bar(n & 1), (n >> 1) & 1, abort, WAIT_LIMIT_NS);
       ptx::tc_fence_after();
       float x[NR];
       const uint32_t s_addr = tmem_base + lane_addr + (n & 1) * NR;
@@ -1015,8 +1066,7 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       any = __any_sync(0xffffffffu, any);   // the same in all four warps
       __syncwarp();
       if (n > 0) {
-        ok = ptx::mbar_wait_bounded(o_bar, (n - 1) & 1, abort, WAIT_LIMIT_NS);   // P and O of tile n - 1
-        if (!ok) break;
+        if (ok) ok = ptx::mbar_wait_bounded(o_bar, (n - 1) & 1, abort, WAIT_LIMIT_NS);   // P and O of tile n - 1
         if (any) {
           ptx::tc_fence_after();
 #pragma unroll
@@ -1061,7 +1111,7 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");
     if (!ok && !*abort) record_timeout(err, abort);
-    if (ok) {
+    {
       ptx::tc_fence_after();
       const long n_rows = (long)a.B * a.Hkv * rows, prow = ((long)b * a.Hkv + hk) * rows;
       const int d = quarter * 32 + lane;       // output dim (HD 64: quarters 0 and 1)

@@ -202,7 +202,9 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      // operand descriptors of the first stage; later ones and K steps by additions (16-byte units)
+      const uint64_t w_desc0 = ptx::smem_desc_sw128(sW), a_desc0 = ptx::smem_desc_sw128(sA);
       int stage = 0, local = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -220,22 +222,31 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t w0 = sW + stage * C::KA * C::ATOM_A, a0 = sA + stage * C::KA * C::ATOM_B;
+          const uint64_t w0 = w_desc0 + (uint64_t)(stage * (C::KA * C::ATOM_A >> 4));
+          const uint64_t a0 = a_desc0 + (uint64_t)(stage * (C::KA * C::ATOM_B >> 4));
+          const uint32_t more = kb != 0 ? 1u : 0u;
+          if (ptx::elect_one()) {
 #pragma unroll
-          for (int k = 0; k < C::KA * 4; ++k)
-            ptx::tc_mma_i8_pair(d_tmem, ptx::smem_desc_sw128(w0 + (k >> 2) * C::ATOM_A + (k & 3) * 32),
-                                ptx::smem_desc_sw128(a0 + (k >> 2) * C::ATOM_B + (k & 3) * 32), C::IDESC,
-                                (kb | k) != 0);
-          ptx::tc_commit_pair(empty_bar(stage), 0x3);
+            for (int k = 0; k < C::KA * 4; ++k)
+              ptx::tc_mma_i8_pair(d_tmem, w0 + (uint64_t)(((k >> 2) * C::ATOM_A + (k & 3) * 32) >> 4),
+                                  a0 + (uint64_t)(((k >> 2) * C::ATOM_B + (k & 3) * 32) >> 4), C::IDESC,
+                                  k != 0 ? 1u : more);
+            ptx::tc_commit_pair(empty_bar(stage), 0x3);
+          }
+          __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        ptx::tc_commit_pair(tfull_bar(acc), 0x3);
+        if (ptx::elect_one()) ptx::tc_commit_pair(tfull_bar(acc), 0x3);
+        __syncwarp();
       }
-      if (!ok && !*abort) record_timeout(err, WHERE_GEMM_MMA, abort);
-      ptx::tc_commit_pair(drain_bar, 0x1);
-      volatile int never = 0;
-      if (!ptx::mbar_wait_bounded(drain_bar, 0, &never, WAIT_LIMIT_NS)) record_timeout(err, WHERE_GEMM_DRAIN, abort);
+      if (ptx::elect_one()) {
+        if (!ok && !*abort) record_timeout(err, WHERE_GEMM_MMA, abort);
+        ptx::tc_commit_pair(drain_bar, 0x1);
+        volatile int never = 0;
+        if (!ptx::mbar_wait_bounded(drain_bar, 0, &never, WAIT_LIMIT_NS)) record_timeout(err, WHERE_GEMM_DRAIN, abort);
+      }
+      __syncwarp();
     }
   } else {
     const int quarter = warp & 3, part = (warp - 2) >> 2;
