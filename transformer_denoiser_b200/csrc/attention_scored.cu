@@ -24,8 +24,11 @@
 // all softmax warps, share a key tile however few the queries are, and an MMA costs N = rows.
 //
 // Keys are split over CTAs while these do not fill the SMs; a second kernel joins the parts.
-// The running maximum is a reference that moves only when it falls 2^8 behind (p stays below
-// 2^8, which fp32 sums and bf16 weights hold as well as 1), so O is rarely rescaled.
+// The weights' reference need not be the running maximum: it only has to keep p = 2^(x - ref) in
+// range, and fp32 sums and bf16 weights hold 2^10 as well as 1.  So a tile's weights are
+// formed with the reference that is there, without its maximum; where their sum (or a cap
+// polynomial's range) shows that this was wrong, and in masked tiles, the maximum is taken,
+// the reference moved and O rescaled.
 //
 // Masked places never reach a result: a masked score is replaced, value rows past kv_len are
 // zeroed in shared memory, and a row whose result is not finite (a NaN or infinity among
@@ -33,6 +36,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "epilogue.cuh"
@@ -51,6 +55,7 @@ constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr int KIMODO_ETIMEOUT_CODE = -5;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_AT = 8.f;            // log2 units the maximum may run ahead of its reference
+constexpr float MAX_SUM = 1024.f;            // weights of 64 keys whose sum stays below need no new one
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -58,78 +63,73 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// cap * tanh(x / cap) in log2 units.  For |x| <= cap: x * R((x / cap)^2) with R(u) = tanh(sqrt u) /
-// sqrt u by a polynomial of degree 5 (weighted least squares towards the relative minimax on
-// [0, 1]; relative error 5.9e-7, on a cap of 50 at most 4e-5 of a weight, a hundredth of its
-// rounding to bf16), which costs no special-function slots: those are what bounds
-// the softmax.  Beyond (rare: the tile is then done again), tanh z = 1 - 2 / (1 + e^(2z)).
-struct CapCoef {
-  float z;               // scale / cap
-  float c[6];            // the polynomial times scale * log2 e
-  float limit;           // |s| up to which it holds
-  float two, cap2;       // e^(2 s z) = 2^(two s); cap * log2 e
-};
-__device__ __forceinline__ CapCoef cap_coef(float scale, float cap) {
-  const float lin = scale * LOG2E;
-  CapCoef k;
-  k.z = scale / cap;
-  k.c[0] = 0.9999994039535522f * lin;
-  k.c[1] = -0.3332904279232025f * lin;
-  k.c[2] = 0.13281433284282684f * lin;
-  k.c[3] = -0.051605645567178726f * lin;
-  k.c[4] = 0.01674308441579342f * lin;
-  k.c[5] = -0.003067048266530037f * lin;
-  k.limit = 1.f / fabsf(k.z);
-  k.two = 2.f * LOG2E * k.z;
+// cap * tanh(x / cap) in log2 units, x = scale s.  For |x| <= cap / 2: s times a polynomial of degree
+// 3 in s^2 for tanh(z) / z (weighted least squares towards the relative minimax on
+// [0, 1/4] in z^2; relative error 5.5e-7, on a cap of 50 at most 2e-5 of a weight, a
+// hundredth of its rounding to bf16).  It costs no special-function slots, which bound
+// the softmax.  Beyond, tanh z = 1 - 2 / (1 + e^(2z)).
+ScoredConst scored_const(float scale, float cap) {
+  const float sc = scale == 0.f ? 1.f : fabsf(scale), lin = sc * LOG2E, z = cap > 0.f ? sc / cap : 0.f;
+  const float r[4] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.044402219355106354f};
+  ScoredConst k;
+  k.lin = make_float2(lin, lin);
+  float f = lin;
+  for (int i = 0; i < 4; ++i) {
+    k.c[i] = make_float2(r[i] * f, r[i] * f);
+    f *= z * z;
+  }
+  // (below 1e-5 the powers of z would leave the floats' range)
+  k.limit2 = z > 1e-5f ? 0.25f / (z * z) : 0.f;
+  k.two = 2.f * LOG2E * z;
   k.cap2 = cap * LOG2E;
   return k;
 }
-// s * ratio = cap * tanh(scale s / cap) in log2 units, two scores at once (f32x2 arithmetic)
-__device__ __forceinline__ float2 cap_ratio(const CapCoef& k, float2 s) {
-  const float2 z = __fmul2_rn(s, make_float2(k.z, k.z));
-  const float2 u = __fmul2_rn(z, z);
-  float2 r = make_float2(k.c[5], k.c[5]);
-#pragma unroll
-  for (int i = 4; i >= 0; --i) r = __ffma2_rn(r, u, make_float2(k.c[i], k.c[i]));
-  return r;
+// two scores at once (f32x2 arithmetic); t = s^2
+__device__ __forceinline__ float2 cap_ratio(const ScoredConst& k, float2 t) {
+  return __ffma2_rn(__ffma2_rn(__ffma2_rn(k.c[3], t, k.c[2]), t, k.c[1]), t, k.c[0]);
 }
-__device__ __forceinline__ float2 capped_poly(const CapCoef& k, float2 s) { return __fmul2_rn(s, cap_ratio(k, s)); }
-__device__ __forceinline__ float capped_any(const CapCoef& k, float s) {
+__device__ __forceinline__ float capped_any(const ScoredConst& k, float s) {
   return fmaf(-2.f * k.cap2, rcp_approx(1.f + ex2(s * k.two)), k.cap2);
 }
+template <int N>
+__device__ __forceinline__ void cap_scores(const ScoredConst& k, float (&x)[N]) {
+  float far = 0.f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) far = fmaxf(far, fabsf(x[e]));
+  if (__any_sync(0xffffffffu, !(far * far <= k.limit2))) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = capped_any(k, x[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const float2 v = make_float2(x[e], x[e + 1]);
+      const float2 y = __fmul2_rn(v, cap_ratio(k, __fmul2_rn(v, v)));
+      x[e] = y.x;
+      x[e + 1] = y.y;
+    }
+  }
+}
 
-// 3-operand maximum and minimum (a NaN operand is passed over, as by fmaxf)
+// 3-operand maximum; a NaN operand gives NaN (and a row whose maximum is NaN is
+// done again at the end)
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 template <int N>
 __device__ __forceinline__ float max_of(const float (&x)[N]) {
-  float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
+  float a[4];
 #pragma unroll
-  for (int e = 4; e < N; e += 4) {
-    a = max3(a, x[e], x[e + 1]);
-    b = max3(b, x[e + 2], x[e + 3]);
-  }
-  return fmaxf(a, b);
-}
-template <int N>
-__device__ __forceinline__ float min_of(const float (&x)[N]) {
-  float a = fminf(x[0], x[1]), b = fminf(x[2], x[3]);
+  for (int c = 0; c < 4; ++c) a[c] = max3(x[c], x[4 + c], x[8 + c]);
 #pragma unroll
-  for (int e = 4; e < N; e += 4) {
-    a = min3(a, x[e], x[e + 1]);
-    b = min3(b, x[e + 2], x[e + 3]);
-  }
-  return fminf(a, b);
+  for (int e = 12; e < N - 4; e += 8)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) a[c] = max3(a[c], x[e + c], x[e + 4 + c]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) a[c] = max3(a[c], x[N - 4 + c], x[N - 4 + c]);
+  return max3(max3(a[0], a[1], a[2]), a[3], a[3]);
 }
-
 __device__ __forceinline__ void record_timeout(DevError* err, volatile int* abort) {
   *abort = 1;
   if (err && atomicCAS(&err->code, 0, KIMODO_ETIMEOUT_CODE) == 0) {
@@ -245,7 +245,8 @@ struct RowTile {
 template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(NUM_THREADS, 1)   // 96 registers a thread
 scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const __grid_constant__ ScoredAttention a, const ScoredPlan plan, DevError* err) {
+                 const __grid_constant__ ScoredAttention a, const __grid_constant__ ScoredPlan plan,
+                 DevError* err) {
   using C = Cfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -261,7 +262,8 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   auto o_bar = [&](int t) { return bar0 + 8u * (2 * STAGES + 4 + t); };   // last P V done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 6);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  RowTile* tiles = reinterpret_cast<RowTile*>(tmem_slot + 2);
+  int* mma_lock = reinterpret_cast<int*>(tmem_slot + 2);
+  RowTile* tiles = reinterpret_cast<RowTile*>(tmem_slot + 4);
   int* docs_smem = reinterpret_cast<int*>(smem + C::BODY + MAX_FLAGS + 256);   // [16 warps][64]
   float* xch = reinterpret_cast<float*>(docs_smem + 16 * 64);                  // [2 turns][2 tiles][2 halves][TILE]
 
@@ -292,6 +294,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     }
     ptx::fence_mbar_init();
     *abort = 0;
+    *mma_lock = 0;
     ptx::tma_prefetch_desc(&tmK);
     ptx::tma_prefetch_desc(&tmV);
   }
@@ -462,7 +465,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, ph, abort, WAIT_LIMIT_NS));
         return ok;
       };
-      auto pv = [&]() {   // O (+)= P V of the pending key tile
+      auto p_ready = [&]() {   // the pending key tile's values and weights
         if (!wait(full_bar(v_stage), v_phase)) return;
         if (v_rows < TILE) {   // value rows past the last key: 0, whatever they hold
           uint8_t* v = smem + 2 * C::Q_BYTES + v_stage * C::KV_BYTES;
@@ -476,18 +479,38 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         if (!wait(p_bar(t), p_phase)) return;
         p_phase ^= 1u;
-        ptx::tc_fence_after();
+      };
+      auto pv = [&]() {   // O (+)= P V of the pending key tile
         const uint32_t v_lo = (uint32_t)d_v + v_stage * (C::KV_BYTES >> 4);
         if (ptx::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < TILE / 16; ++kk)
-            ptx::tc_mma_bf16_ta_lo(o_tmem, s_tmem + kk * 8, v_lo + kk * (2048 >> 4), v_hi, idesc_o,
+            ptx::tc_mma_bf16_ta_lo(o_tmem, s_tmem + (kk >> 2) * 64 + (kk & 3) * 8, v_lo + kk * (2048 >> 4), v_hi, idesc_o,
                                    kk != 0 ? 1u : started);
           ptx::tc_commit(empty_bar(v_stage));
         }
         __syncwarp();
         started = 1u;
         pend = false;
+      };
+      // The two warps take turns in whole blocks (P V and Q K^T of one tile): interleaved, both
+      // tiles' scores would come at the same time, and softmax and tensor cores would wait for
+      // each other instead of working on one tile each.
+      auto lock = [&]() {
+        if (lane == 0) {
+          const uint64_t t0 = ptx::global_timer_ns();
+          while (atomicCAS(mma_lock, 0, 1) != 0)
+            if (*abort || ptx::global_timer_ns() - t0 > WAIT_LIMIT_NS) {
+              if (!*abort) record_timeout(err, abort);
+              break;
+            }
+        }
+        __syncwarp();
+        ptx::tc_fence_after();
+      };
+      auto unlock = [&]() {
+        __syncwarp();
+        if (lane == 0) atomicExch(mma_lock, 0);
       };
       for (int jt = jt0; jt < jt1; ++jt) {
         const bool mine = __shfl_sync(0xffffffffu, (int)takes(t, jt), 0) != 0;
@@ -498,26 +521,31 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         if (mine && !wait(full_bar(k_stage), k_phase)) break;
         if (pend) {
-          pv();
+          p_ready();
           if (!ok) break;
         }
-        if (mine) {
-          ptx::tc_fence_after();
-          const uint32_t k_lo = (uint32_t)d_k + k_stage * (C::KV_BYTES >> 4);
-          if (ptx::elect_one()) {
+        if (mine || pend) {
+          lock();
+          if (pend) pv();
+          if (mine) {
+            const uint32_t k_lo = (uint32_t)d_k + k_stage * (C::KV_BYTES >> 4);
+            if (ptx::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk)
-              ptx::tc_mma_bf16_lo(s_tmem, q_lo + (((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4),
-                                  k_lo + (((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4), k_hi, idesc_s, kk != 0);
-            ptx::tc_commit(s_bar(t));
-            ptx::tc_commit(empty_bar(k_stage));
+              for (int kk = 0; kk < HD / 16; ++kk)
+                ptx::tc_mma_bf16_lo(s_tmem, q_lo + (((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4),
+                                    k_lo + (((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4), k_hi, idesc_s, kk != 0);
+              ptx::tc_commit(s_bar(t));
+              ptx::tc_commit(empty_bar(k_stage));
+            }
+            __syncwarp();
+            pend = true;
+            v_stage = stage;
+            v_phase = phase;
+            v_rows = min(seq.kv_len - jt * TILE, TILE);
           }
-          __syncwarp();
-          pend = true;
-          v_stage = stage;
-          v_phase = phase;
-          v_rows = min(seq.kv_len - jt * TILE, TILE);
-        } else {   // the other tile's alone: hand both stages on, once they have been filled
+          unlock();
+        }
+        if (!mine) {   // the other tile's alone: hand both stages on, once they have been filled
           if (!wait(full_bar(k_stage), k_phase) || !wait(full_bar(stage), phase)) break;
           if (lane == 0) {
             ptx::mbar_arrive(empty_bar(k_stage));
@@ -526,7 +554,14 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      if (ok && pend) pv();
+      if (ok && pend) {
+        p_ready();
+        if (ok) {
+          lock();
+          pv();
+          unlock();
+        }
+      }
       if (!ok && !*abort && lane == 0) record_timeout(err, abort);
       if (ptx::elect_one()) {
         ptx::tc_commit(o_bar(t));
@@ -550,14 +585,9 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const int p = seq.start + i_own;
     const int last = row_ok ? last_key(a, seq, (long)seq.start + i_own) : -1;
     const float slope2 = BIAS && row_ok ? a.slopes[hk * a.G + g_own] * LOG2E : 0.f;
-    // Scores grow with the raw product (after its sign is that of the scale) where there is no
-    // bias; a scale of 0 is a product of 0.
-    const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
-    const CapCoef cc = cap_coef(scale, CAP ? a.cap : 1.f);
-    // Without cap and bias the scale is applied with the reference's subtraction (one FMA), so
-    // the maximum is taken of the raw scores.
-    constexpr bool RAW = !CAP && !BIAS;
-    const float sc = scale * LOG2E;
+    // the constants are those of |scale|: the products take its sign, and a scale of 0 is products of 0
+    const ScoredConst& cc = plan.k;
+    const float sc = cc.lin.x;
     const int* kdocs = docs ? a.kv_doc + (long)b * a.Sk : nullptr;
     int* dbuf = docs_smem + (warp - 4) * KH;
     float m = -INFINITY;            // reference of the weights (log2 units)
@@ -587,98 +617,123 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
           for (int e = 0; e < KH; ++e) x[e] = a.scale < 0.f ? -x[e] : 0.f;
         }
-        const bool masked = !one_doc || !__all_sync(0xffffffffu, j0 + KH - 1 <= last || !row_ok);
-        float top = RAW ? 0.f : max_of(x);
-        bool direct = false;   // CAP alone: x stays raw, the cap is applied with the reference
-        if constexpr (CAP) {
-          const bool near = !__any_sync(0xffffffffu, !(fmaxf(top, -min_of(x)) <= cc.limit));
-          direct = !BIAS && near && !masked;
-          if (direct) {
-            top = capped_poly(cc, make_float2(top, top)).x;
-          } else if (near) {
-#pragma unroll
-            for (int e = 0; e < KH; e += 2) {
-              const float2 y = capped_poly(cc, make_float2(x[e], x[e + 1]));
-              x[e] = y.x;
-              x[e + 1] = y.y;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < KH; ++e) x[e] = capped_any(cc, x[e]);
-          }
-        }
-        if constexpr (BIAS) {
-          const float d0 = (float)(p - j0);
-#pragma unroll
-          for (int e = 0; e < KH; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), CAP ? x[e] : x[e] * sc);
-        }
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < KH; ++e)
-            if (j0 + e > last) x[e] = -INFINITY;
-          if (!one_doc) {
-#pragma unroll
-            for (int e = 0; e < KH; e += 4) {
-              const int4 d = *reinterpret_cast<const int4*>(dbuf + e);
-              if (d.x != qdoc || qdoc < 0) x[e] = -INFINITY;
-              if (d.y != qdoc || qdoc < 0) x[e + 1] = -INFINITY;
-              if (d.z != qdoc || qdoc < 0) x[e + 2] = -INFINITY;
-              if (d.w != qdoc || qdoc < 0) x[e + 3] = -INFINITY;
-            }
-          }
-        }
-        if (!direct) top = max_of(x);
-        if (RAW) top *= sc;
-        // the other half's maximum
         float* xm = xch + ((phase * 2 + t) * 2) * TILE;
-        xm[half * TILE + lrow] = top;
-        pair_sync();
-        top = fmaxf(top, xm[(half ^ 1) * TILE + lrow]);
-        // move the reference: at once while there is none, later only when it falls far behind
-        const bool move = !started || top > m + RESCALE_AT;
-        const float m_new = move ? fmaxf(m, top) : m;
-        if (started && __any_sync(0xffffffffu, move)) {   // both warps of the rows alike
-          const float f = m_new == m ? 1.f : ex2(m - m_new);   // m = -infinity: 0
-          l2.x *= f;
-          l2.y *= f;
-#pragma unroll 1
-          for (int c = half * DH2; c < (half + 1) * DH2; c += 16) {
-            float v[16];
-            uint32_t w[16];
-            ptx::tmem_ld(o_addr + c, v);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * f);
-            ptx::tmem_st16(o_addr + c, w);
-          }
-        }
-        m = m_new;
-        const float ref = m == -INFINITY ? 0.f : m;
-        const float2 nref2 = make_float2(-ref, -ref), sc2 = make_float2(sc, sc);
-        // weights over the scores: this half's 64 in 32 columns (the other half has read its own)
+        // the weights arg(score pair) of this half's 64 keys, in bf16 in the first 32 of their columns
         auto weights = [&](auto arg) {
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < KH; c += 32) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 y = arg(make_float2(x[c + e], x[c + e + 1]));
+              const float2 y = arg(make_float2(x[c + e], x[c + e + 1]), c + e);
               const float2 pw = make_float2(ex2(y.x), ex2(y.y));
-              l2 = __fadd2_rn(l2, pw);
+              sum = __fadd2_rn(sum, pw);
               w[e / 2] = bf16x2_bits(pw.x, pw.y);
             }
-            ptx::tmem_st16(s_addr + half * (KH / 2) + c / 2, w);
+            ptx::tmem_st16(s_addr + half * KH + c / 2, w);
           }
+          return sum;
         };
-        if (RAW) {
-          weights([&](float2 v) { return __ffma2_rn(v, sc2, nref2); });
-        } else if (CAP && !BIAS) {
-          if (direct)
-            weights([&](float2 v) { return __ffma2_rn(v, cap_ratio(cc, v), nref2); });
+        // both warps of the rows decide alike: the conditions are those of the rows
+        const bool masked = !one_doc || !__all_sync(0xffffffffu, jt * TILE + TILE - 1 <= last || !row_ok);
+        bool done = false, tried = false;
+        if (!masked && __all_sync(0xffffffffu, m > -INFINITY || !row_ok)) {
+          const float2 nref2 = make_float2(-m, -m);
+          float2 sum;
+          float far = 0.f;
+          if constexpr (CAP) {
+            if constexpr (BIAS) {
+              // -slope |p - j| is linear in j on either side of p; a tile that p cuts takes the other way
+              const float d0 = (float)(p - j0), sl = d0 > 0.f ? -slope2 : slope2;
+              far = d0 < (float)KH && d0 > 0.f ? INFINITY : 0.f;
+              const float2 sl2 = make_float2(-sl, -sl), b2 = make_float2(fmaf(sl, d0, -m), fmaf(sl, d0, -m));
+              sum = weights([&](float2 v, int e) {
+                const float2 u = __fmul2_rn(v, v);
+                far = max3(far, u.x, u.y);
+                return __ffma2_rn(v, cap_ratio(cc, u), __ffma2_rn(sl2, make_float2((float)e, (float)(e + 1)), b2));
+              });
+            } else {
+              sum = weights([&](float2 v, int) {
+                const float2 u = __fmul2_rn(v, v);
+                far = max3(far, u.x, u.y);
+                return __ffma2_rn(v, cap_ratio(cc, u), nref2);
+              });
+            }
+          } else if constexpr (BIAS) {
+            const float d0 = (float)(p - j0), sl = d0 > 0.f ? -slope2 : slope2;
+            far = d0 < (float)KH && d0 > 0.f ? INFINITY : 0.f;
+            const float2 sl2 = make_float2(-sl, -sl), b2 = make_float2(fmaf(sl, d0, -m), fmaf(sl, d0, -m));
+            sum = weights([&](float2 v, int e) {
+              return __ffma2_rn(v, cc.lin, __ffma2_rn(sl2, make_float2((float)e, (float)(e + 1)), b2));
+            });
+          } else {
+            sum = weights([&](float2 v, int) { return __ffma2_rn(v, cc.lin, nref2); });
+          }
+          const bool good = sum.x + sum.y <= MAX_SUM && far <= (CAP ? cc.limit2 : 0.f);
+          const bool all_good = __all_sync(0xffffffffu, good || !row_ok);
+          if (lane == 0) xm[half * TILE + lrow] = all_good ? 1.f : 0.f;
+          pair_sync();
+          done = all_good && xm[(half ^ 1) * TILE + (lrow & ~31)] != 0.f;
+          tried = true;
+          if (done)
+            l2 = __fadd2_rn(l2, sum);
           else
-            weights([&](float2 v) { return __fadd2_rn(v, nref2); });
-        } else {
-          weights([&](float2 v) { return __fadd2_rn(v, nref2); });
+            pair_sync();   // the flags have been read: the maxima go to the same place
+        }
+        if (!done) {
+          if constexpr (CAP)
+            cap_scores(cc, x);
+          else {
+#pragma unroll
+            for (int e = 0; e < KH; ++e) x[e] *= sc;
+          }
+          if constexpr (BIAS) {
+            const float d0 = (float)(p - j0);
+#pragma unroll
+            for (int e = 0; e < KH; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), x[e]);
+          }
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < KH; ++e)
+              if (j0 + e > last) x[e] = -INFINITY;
+            if (!one_doc) {
+#pragma unroll
+              for (int e = 0; e < KH; e += 4) {
+                const int4 d = *reinterpret_cast<const int4*>(dbuf + e);
+                if (d.x != qdoc || qdoc < 0) x[e] = -INFINITY;
+                if (d.y != qdoc || qdoc < 0) x[e + 1] = -INFINITY;
+                if (d.z != qdoc || qdoc < 0) x[e + 2] = -INFINITY;
+                if (d.w != qdoc || qdoc < 0) x[e + 3] = -INFINITY;
+              }
+            }
+          }
+          xm[half * TILE + lrow] = max_of(x);
+          pair_sync();
+          const float top = max3(xm[lrow], xm[TILE + lrow], m);
+          // move the reference: at once while there is none or where it did not do, else only when
+          // it falls far behind
+          const bool move = !started || !(top <= (tried ? m : m + RESCALE_AT));
+          const float m_new = move ? top : m;
+          if (started && __any_sync(0xffffffffu, move)) {   // both warps of the rows alike
+            const float f = m_new == m ? 1.f : ex2(m - m_new);   // m = -infinity: 0
+            l2.x *= f;
+            l2.y *= f;
+#pragma unroll 1
+            for (int c = half * DH2; c < (half + 1) * DH2; c += 16) {
+              float v[16];
+              uint32_t w[16];
+              ptx::tmem_ld(o_addr + c, v);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * f);
+              ptx::tmem_st16(o_addr + c, w);
+            }
+          }
+          m = m_new;
+          const float ref = m == -INFINITY ? 0.f : m;
+          const float2 nref2 = make_float2(-ref, -ref);
+          l2 = __fadd2_rn(l2, weights([&](float2 v, int) { return __fadd2_rn(v, nref2); }));
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
@@ -791,7 +846,8 @@ __device__ __forceinline__ float warp_max(float v) {
 template <int HD, int NR>
 __global__ void __launch_bounds__(F_THREADS, NR == 16 ? 2 : 1)
 scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const __grid_constant__ ScoredAttention a, const ScoredPlan plan, DevError* err) {
+                  const __grid_constant__ ScoredAttention a, const __grid_constant__ ScoredPlan plan,
+                  DevError* err) {
   using C = FewCfg<HD, NR>;
   constexpr int NST = C::NST;
   extern __shared__ uint8_t smem_raw[];
@@ -976,8 +1032,8 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const uint32_t o_addr = tmem_base + lane_addr + 2 * NR;
     constexpr int RL = (NR + 31) / 32;          // rows kept per lane
     const bool cap = a.cap > 0.f, bias = a.slopes != nullptr, docs = a.q_doc != nullptr;
-    const CapCoef cc = cap_coef(a.scale, cap ? a.cap : 1.f);
-    const float sc = a.scale * LOG2E;
+    const ScoredConst& cc = plan.k;
+    const float sc = a.scale == 0.f ? 0.f : copysignf(cc.lin.x, a.scale);
     const int all_see = row_last[0];            // keys up to here are seen by every row
     float* refs = wref + sw * 2 * NR;
     float* facs = refs + NR;
@@ -1004,19 +1060,10 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       }
       ptx::tmem_ld_wait();
       if (cap) {
-        float far = 0.f;
+        cap_scores(cc, x);
+        if (a.scale <= 0.f) {   // the constants are those of |scale|
 #pragma unroll
-        for (int r = 0; r < NR; ++r) far = fmaxf(far, fabsf(x[r]));
-        if (__any_sync(0xffffffffu, !(far <= cc.limit))) {
-#pragma unroll
-          for (int r = 0; r < NR; ++r) x[r] = capped_any(cc, x[r]);
-        } else {
-#pragma unroll
-          for (int r = 0; r < NR; r += 2) {
-            const float2 y = capped_poly(cc, make_float2(x[r], x[r + 1]));
-            x[r] = y.x;
-            x[r + 1] = y.y;
-          }
+          for (int r = 0; r < NR; ++r) x[r] = a.scale < 0.f ? -x[r] : 0.f;
         }
       } else {
 #pragma unroll
@@ -1499,6 +1546,7 @@ ScoredPlan scored_attention_plan(const ScoredAttention& a, bool is_bf16, int num
     fill = 3;
     least = 4;
   }
+  p.k = scored_const(a.scale, a.cap);
   p.row_blocks = (int)((rows + block - 1) / block);
   const int key_tiles = (a.Sk + tile - 1) / tile;
   const long ctas = (long)p.row_blocks * a.Hkv * a.B, want = (long)fill * num_sms;

@@ -170,11 +170,20 @@ struct ScoredAttention {
   float scale = 0.f, cap = 0.f;
   int causal = 0;
 };
+// What the kernels multiply scores by, as pairs (f32x2 operands); computed on the host, so that
+// it sits in constant memory and not in the softmax threads' registers.
+struct ScoredConst {
+  float2 lin;            // |scale| * log2 e (a scale of 0 counts as 1: its scores are made 0)
+  float2 c[4];           // tanh(z) / z * lin as a polynomial in s^2, z = |scale| s / cap
+  float limit2;          // s^2 up to which it holds
+  float two, cap2;       // e^(2 z) = 2^(two s); cap * log2 e
+};
 // Split of a call over CTAs and keys; parts > 1: results of each part and their weights in a
 // workspace of `bytes`, joined by a second kernel.
 struct ScoredPlan {
   int splits = 1, tiles_per_split = 1, row_blocks = 1, parts = 1;
   int few = 0;   // rows of the kernels for few rows (0: not those)
+  ScoredConst k;
   float* part_o = nullptr;
   float* part_lse = nullptr;
   size_t bytes = 0;
