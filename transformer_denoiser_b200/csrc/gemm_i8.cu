@@ -11,6 +11,8 @@
 // nothing.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
 #include <type_traits>
 
 #include "common.cuh"
@@ -45,19 +47,26 @@ __device__ __forceinline__ void record_timeout(DevError* err, int where, volatil
   }
 }
 
+// Residual of channel n for the tokens m0 .. m0 + NV - 1, loaded before the accumulators are there.
+template <int KIND, int NV>
+__device__ __forceinline__ void load_resid(const I8Epi& e, int n, int m0, float (&r)[NV]) {
+  if constexpr (KIND == EPI_BIAS_RESID) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) r[j] = n < e.N && m0 + j < e.M ? e.resid[(long)(m0 + j) * e.ldr + n] : 0.f;
+  }
+}
+
 // Finish and store the accumulators v (32-bit integers) of channel n for the tokens
 // m0 .. m0 + NV - 1; sm: lane l holds the scale of token m0 + l.
 template <int KIND, typename OutT, int NV>
 __device__ __forceinline__ void store_tokens(const I8Epi& e, int n, float sn, float bn, int m0, float sm,
-                                             const int (&v)[NV]) {
+                                             const int (&v)[NV], const float (&r)[NV]) {
   const bool col = n < e.N;
   float y[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) y[j] = fmaf((float)v[j], __shfl_sync(0xffffffffu, sm, j) * sn, bn);
-  if constexpr (KIND == EPI_BIAS_RESID) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (col && m0 + j < e.M) y[j] += e.resid[(long)(m0 + j) * e.ldr + n];
+  for (int j = 0; j < NV; ++j) {
+    y[j] = fmaf((float)v[j], __shfl_sync(0xffffffffu, sm, j) * sn, bn);
+    if constexpr (KIND == EPI_BIAS_RESID) y[j] += r[j];
   }
   if constexpr (KIND == EPI_BIAS_GELU) {
 #pragma unroll
@@ -95,7 +104,7 @@ struct PairCfg {
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + NUM_BARS * 8 + 16;
   static constexpr uint32_t TMEM_COLS = 2 * BN <= 32 ? 32 : 2 * BN <= 64 ? 64 : 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;
   static constexpr uint32_t IDESC = ptx::idesc_i8_s32(256, BN);
-  static_assert(BN % 64 == 0 && BN <= 256, "whole 32-token chunks for each epilogue half");
+  static_assert(BN % 32 == 0 && BN <= 256, "MMA N of the pair, whole 32-token chunks");
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -260,6 +269,9 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
       const int n = w * 256 + (int)rank * 128 + quarter * 32 + lane;
       const float sn = n < ep.N ? ep.w_scale[n] : 0.f;
       const float bn = n < ep.N && ep.bias != nullptr ? ep.bias[n] : 0.f;
+      // 32-token chunks part, part + 2, ...; the residual of a chunk is loaded a chunk ahead
+      float res[32];
+      load_resid<KIND>(ep, n, t * BN + part * 32, res);
       if (!ptx::mbar_wait_bounded(tfull_bar(acc), (local >> 1) & 1, abort, WAIT_LIMIT_NS)) {
         if (!*abort) record_timeout(err, WHERE_GEMM_EPILOGUE, abort);
         break;
@@ -267,17 +279,20 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN;
 #pragma unroll 1
-      for (int c = part * (BN / 2); c < (part + 1) * (BN / 2); c += 32) {
+      for (int c = part * 32; c < BN; c += 64) {
         const int m0 = t * BN + c;
         if (m0 >= ep.M) break;
         const float sm = m0 + lane < ep.M ? ep.a_scale[m0 + lane] : 0.f;
-        float f[32];
+        float f[32], now[32];
         int v[32];
         ptx::tmem_ld(taddr + c, f);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) now[j] = res[j];
+        if (c + 64 < BN) load_resid<KIND>(ep, n, m0 + 64, res);
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __float_as_int(f[j]);
-        store_tokens<KIND, OutT, 32>(ep, n, sn, bn, m0, sm, v);
+        store_tokens<KIND, OutT, 32>(ep, n, sn, bn, m0, sm, v, now);
       }
       ptx::tc_fence_before();
       __syncwarp();
@@ -291,6 +306,188 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ====================================================================== single CTAs (few tokens)
+//
+// One CTA computes `ct` channels x BN tokens over the whole K.  With few tokens the time is that of
+// the weights' bytes, and one SM takes in about 60 bytes a cycle, so the channels are cut as
+// narrow as gives every SM a CTA (1 x 4096 x 4096: 128 CTAs of 32 channels), with the whole
+// ring of stages in flight.  The MMA still has 128 rows; those past ct read whatever follows in
+// shared memory and are not looked at.  (Slices of K over a cluster, exchanged through
+// distributed shared memory, measured 9.2 us there against 7.9 us for one CTA of 128
+// channels and all of K.)
+// Roles (192 threads): warp 0 TMA, warp 1 MMA, warps 2-5 epilogue.
+constexpr int S_THREADS = 192;
+constexpr int S_MAX_STAGES = 16;
+constexpr uint32_t S_SMEM_MAX = 232448;
+struct SmallPlan {
+  int ct;        // channels of a CTA: 16, 32, 64 or 128
+  int ka;        // 128-column blocks of a stage
+  int stages;
+  int num_kb;    // blocks of K, the last one perhaps partial
+  int whole;     // whole blocks
+};
+__host__ __device__ inline uint32_t small_stage_bytes(const SmallPlan& p, int bn) {
+  return (uint32_t)p.ka * (uint32_t)(p.ct + bn) * 128;
+}
+// behind the stages, room for the rows past ct of the last one's MMAs, then barriers
+__host__ __device__ inline uint32_t small_pad_bytes(const SmallPlan& p) { return (uint32_t)(128 - p.ct) * 128; }
+inline size_t small_smem(const SmallPlan& p, int bn) {
+  return 1024 + (size_t)p.stages * small_stage_bytes(p, bn) + small_pad_bytes(p) + (2 * S_MAX_STAGES + 1) * 8 + 16;
+}
+
+template <int BN, int KIND, typename OutT>
+__global__ void __launch_bounds__(S_THREADS)
+gemm_i8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ CUtensorMap tmWt, const __grid_constant__ CUtensorMap tmAt, SmallPlan p,
+                     I8Epi ep, DevError* err) {
+  constexpr uint32_t COLS = BN <= 32 ? 32 : BN <= 64 ? 64 : 128;
+  constexpr uint32_t IDESC = ptx::idesc_i8_s32(128, BN);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t atom_w = (uint32_t)p.ct * 128, atom_a = BN * 128;
+  // token stages first: what the weight stages' MMAs read past ct rows lies behind them
+  const uint32_t sA = ptx::smem_u32(smem), sW = sA + p.stages * p.ka * atom_a;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.stages * small_stage_bytes(p, BN) + small_pad_bytes(p));
+  const uint32_t bar0 = ptx::smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S_MAX_STAGES + s); };
+  const uint32_t done_bar = bar0 + 8u * (2 * S_MAX_STAGES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S_MAX_STAGES + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = blockIdx.x * p.ct, t0 = blockIdx.y * BN;
+  const int steps = (p.num_kb + p.ka - 1) / p.ka;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    ptx::mbar_init(done_bar, 1);
+    ptx::fence_mbar_init();
+    *abort = 0;
+    ptx::tma_prefetch_desc(&tmW);
+    ptx::tma_prefetch_desc(&tmA);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::pdl_wait();
+  ptx::pdl_trigger();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = 0; i < steps; ++i) {
+        if (i >= p.stages) {
+          ok = ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort, WAIT_LIMIT_NS);
+          if (!ok) break;
+        }
+        const int kb = i * p.ka, n = min(p.ka, p.num_kb - kb);
+        const uint32_t dw = sW + stage * p.ka * atom_w, da = sA + stage * p.ka * atom_a;
+        ptx::mbar_arrive_expect_tx(full_bar(stage), (uint32_t)n * (atom_w + atom_a));
+        if (kb + p.ka <= p.whole) {   // whole blocks only: one box an operand
+          ptx::tma_load_3d(dw, &tmW, full_bar(stage), 0, n0, kb);
+          ptx::tma_load_3d(da, &tmA, full_bar(stage), 0, t0, kb);
+        } else {
+          for (int a = 0; a < n; ++a) {
+            ptx::tma_load_2d(dw + a * atom_w, &tmWt, full_bar(stage), (kb + a) * BK, n0);
+            ptx::tma_load_2d(da + a * atom_a, &tmAt, full_bar(stage), (kb + a) * BK, t0);
+          }
+        }
+        ++issued;
+        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) {
+        if (!*abort) record_timeout(err, WHERE_GEMM_PRODUCER, abort);
+        volatile int never = 0;   // every copy issued has landed before the CTA leaves
+        for (int i = 0; i < issued && i < p.stages; ++i) {
+          if (--stage < 0) { stage = p.stages - 1; phase ^= 1u; }
+          ptx::mbar_wait_bounded(full_bar(stage), phase, &never, WAIT_LIMIT_NS);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    const uint64_t w_desc0 = ptx::smem_desc_sw128(sW), a_desc0 = ptx::smem_desc_sw128(sA);
+    int stage = 0;
+    uint32_t phase = 0, more = 0;
+    bool ok = true;
+    for (int i = 0; i < steps; ++i) {
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(full_bar(stage), phase, abort, WAIT_LIMIT_NS));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const int n = min(p.ka, p.num_kb - i * p.ka);
+      for (int a = 0; a < n; ++a) {
+        const uint64_t w0 = w_desc0 + (uint64_t)((stage * p.ka + a) * (atom_w >> 4));
+        const uint64_t a0 = a_desc0 + (uint64_t)((stage * p.ka + a) * (atom_a >> 4));
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            ptx::tc_mma_i8(tmem_base, w0 + (uint64_t)(k * 2), a0 + (uint64_t)(k * 2), IDESC, k != 0 ? 1u : more);
+        }
+        __syncwarp();
+        more = 1u;
+      }
+      if (ptx::elect_one()) ptx::tc_commit(empty_bar(stage));
+      __syncwarp();
+      if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+    }
+    if (ptx::elect_one()) {
+      if (!ok && !*abort) record_timeout(err, WHERE_GEMM_MMA, abort);
+      ptx::tc_commit(done_bar);
+      volatile int never = 0;
+      if (!ptx::mbar_wait_bounded(done_bar, 0, &never, WAIT_LIMIT_NS)) record_timeout(err, WHERE_GEMM_DRAIN, abort);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    if (quarter * 32 < p.ct) {   // whole warps past the channels have nothing to do
+      const int n = row < p.ct ? n0 + row : ep.N;   // ep.N: no channel
+      const float sn = n < ep.N ? ep.w_scale[n] : 0.f;
+      const float bn = n < ep.N && ep.bias != nullptr ? ep.bias[n] : 0.f;
+      constexpr int CH = BN % 32 == 0 ? 32 : 16;   // tokens of a chunk; its residual is loaded a chunk ahead
+      float res[CH];
+      load_resid<KIND>(ep, n, t0, res);
+      const float sm0 = lane < CH && t0 + lane < ep.M ? ep.a_scale[t0 + lane] : 0.f;
+      const bool ok = ptx::mbar_wait_bounded(done_bar, 0, abort, WAIT_LIMIT_NS);
+      if (!ok && !*abort) record_timeout(err, WHERE_GEMM_EPILOGUE, abort);
+      ptx::tc_fence_after();
+      if (__all_sync(0xffffffffu, ok)) {
+        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < BN; c += CH) {
+          const int m0 = t0 + c;
+          if (m0 >= ep.M) break;
+          const float sm = c == 0 ? sm0 : lane < CH && m0 + lane < ep.M ? ep.a_scale[m0 + lane] : 0.f;
+          float f[CH], now[CH];
+          int v[CH];
+          ptx::tmem_ld(taddr + c, f);
+#pragma unroll
+          for (int j = 0; j < CH; ++j) now[j] = res[j];
+          if (c + CH < BN) load_resid<KIND>(ep, n, m0 + CH, res);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < CH; ++j) v[j] = __float_as_int(f[j]);
+          store_tokens<KIND, OutT, CH>(ep, n, sn, bn, m0, sm, v, now);
+        }
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, COLS);
   }
 }
 
@@ -326,12 +523,90 @@ cudaError_t launch_pair(const GemmI8& g, const I8Epi& ep, DevError* err, cudaStr
   return cudaLaunchKernelEx(&cfg, kern, tw, ta, nw, nt, (g.K + C::KA * BK - 1) / (C::KA * BK), ep, err);
 }
 
+template <int BN, int KIND, typename OutT>
+cudaError_t launch_small(const GemmI8& g, const I8Epi& ep, int ct, DevError* err, cudaStream_t st) {
+  SmallPlan p;
+  p.ct = ct;
+  p.num_kb = (g.K + BK - 1) / BK;
+  p.whole = g.K / BK;
+  p.ka = ct + BN <= 64 ? 4 : ct + BN <= 128 ? 2 : 1;   // 16 to 32 KB a stage
+  const int steps = (p.num_kb + p.ka - 1) / p.ka;
+  const long room = (long)S_SMEM_MAX - 1024 - small_pad_bytes(p) - (2 * S_MAX_STAGES + 1) * 8 - 16;
+  p.stages = (int)(room / small_stage_bytes(p, BN));
+  if (p.stages > S_MAX_STAGES) p.stages = S_MAX_STAGES;
+  if (p.stages > steps) p.stages = steps;
+  auto kern = gemm_i8_small_kernel<BN, KIND, OutT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S_SMEM_MAX);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tw, ta, twt, tat;
+  if (make_tmap_i8(&twt, g.W, g.N, g.K, g.ldw, ct) || make_tmap_i8(&tat, g.A, g.M, g.K, g.lda, BN))
+    return cudaErrorInvalidValue;
+  tw = twt;
+  ta = tat;
+  if (p.whole > 0 && (make_tmap_i8_blocks(&tw, g.W, g.N, g.K, g.ldw, ct, p.ka) ||
+                      make_tmap_i8_blocks(&ta, g.A, g.M, g.K, g.lda, BN, p.ka)))
+    return cudaErrorInvalidValue;
+  return launch_kernel(kern, dim3((unsigned)((g.N + ct - 1) / ct), (unsigned)((g.M + BN - 1) / BN)), dim3(S_THREADS),
+                       small_smem(p, BN), st, tw, ta, twt, tat, p, ep, err);
+}
+
+// Tile and kernel of a call, by estimated cycles.  An SM takes about 48 bytes a cycle from L2 and
+// does 16384 8-bit MMA operations; a 32-token chunk of an epilogue warp takes about 1500
+// cycles, and a tile's set-up and first loads 3000.
+struct Choice {
+  bool pair;
+  int bn, ct;
+};
+Choice choose(int M, int N, int K, int num_sms) {
+  const double atoms = (K + BK - 1) / BK;
+  Choice best{true, 256, 256};
+  double least = 1e30;
+  auto offer = [&](double cost, Choice c) {
+    if (cost < least) {
+      least = cost;
+      best = c;
+    }
+  };
+  for (int bn : {64, 96, 128, 160, 192, 224, 256}) {
+    const double tiles = (double)((N + 255) / 256) * ((M + bn - 1) / bn);
+    const double rounds = ceil(tiles / (num_sms / 2));
+    const double main = atoms * fmax(2.0 * bn, (16384 + 64.0 * bn) / 48), epi = 500 + 1500.0 * ((bn + 63) / 64);
+    offer(3000 + rounds * fmax(main, epi) + epi, Choice{true, bn, 256});
+  }
+  for (int bn : {16, 32, 48, 64, 96, 128})
+    for (int ct : {16, 32, 64, 128}) {
+      if ((M + bn - 1) / bn > 65535) continue;
+      const double tiles = (double)((N + ct - 1) / ct) * ((M + bn - 1) / bn);
+      const double rounds = ceil(tiles / num_sms);
+      const double main = atoms * fmax(4.0 * bn, 128.0 * (ct + bn) / 48), epi = 500 + 1500.0 * ((bn + 31) / 32);
+      offer(rounds * (3000 + main + epi), Choice{false, bn, ct});
+    }
+  return best;
+}
+
 template <int KIND, typename OutT>
 cudaError_t run(const GemmI8& g, DevError* err, cudaStream_t st, int num_sms) {
   I8Epi ep{g.a_scale, g.w_scale, g.bias, g.resid, g.ldr, g.out, g.ldo, g.M, g.N};
-  if (g.M <= 64) return launch_pair<64, KIND, OutT>(g, ep, err, st, num_sms);
-  if (g.M <= 2048) return launch_pair<128, KIND, OutT>(g, ep, err, st, num_sms);
-  return launch_pair<256, KIND, OutT>(g, ep, err, st, num_sms);
+  const Choice c = choose(g.M, g.N, g.K, num_sms);
+  if (c.pair) {
+    switch (c.bn) {
+      case 64: return launch_pair<64, KIND, OutT>(g, ep, err, st, num_sms);
+      case 96: return launch_pair<96, KIND, OutT>(g, ep, err, st, num_sms);
+      case 128: return launch_pair<128, KIND, OutT>(g, ep, err, st, num_sms);
+      case 160: return launch_pair<160, KIND, OutT>(g, ep, err, st, num_sms);
+      case 192: return launch_pair<192, KIND, OutT>(g, ep, err, st, num_sms);
+      case 224: return launch_pair<224, KIND, OutT>(g, ep, err, st, num_sms);
+      default: return launch_pair<256, KIND, OutT>(g, ep, err, st, num_sms);
+    }
+  }
+  switch (c.bn) {
+    case 16: return launch_small<16, KIND, OutT>(g, ep, c.ct, err, st);
+    case 32: return launch_small<32, KIND, OutT>(g, ep, c.ct, err, st);
+    case 48: return launch_small<48, KIND, OutT>(g, ep, c.ct, err, st);
+    case 64: return launch_small<64, KIND, OutT>(g, ep, c.ct, err, st);
+    case 96: return launch_small<96, KIND, OutT>(g, ep, c.ct, err, st);
+    default: return launch_small<128, KIND, OutT>(g, ep, c.ct, err, st);
+  }
 }
 
 }  // namespace

@@ -385,6 +385,23 @@ int make_tmap_i8(CUtensorMap* m, const void* base, int rows, int cols, long ld, 
   return r == CUDA_SUCCESS ? 0 : -3;
 }
 
+// The same matrix as whole 128-column blocks: boxes of `blocks` blocks x box_rows rows, block
+// after block in shared memory (each as make_tmap_i8 lays it out).  Coordinates (0, row,
+// block); columns past the last whole block are not covered.
+int make_tmap_i8_blocks(CUtensorMap* m, const void* base, int rows, int cols, long ld, int box_rows, int blocks) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return -1;
+  if ((reinterpret_cast<uintptr_t>(base) & 15) || ld % 16) return -2;
+  cuuint64_t dims[3] = {128, (cuuint64_t)rows, (cuuint64_t)(cols / 128)};
+  cuuint64_t strides[2] = {(cuuint64_t)ld, 128};
+  cuuint32_t box[3] = {128, (cuuint32_t)box_rows, (cuuint32_t)blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -3;
+}
+
 // Keys or values bf16 [batch][token][head][dims] with any strides (elements, multiples of 8;
 // the dims consecutive): boxes of 64 dims x 128 tokens, 128-byte swizzle, zero fill.  The
 // coordinates are (dim, token, head, sequence).

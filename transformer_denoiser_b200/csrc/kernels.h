@@ -147,6 +147,7 @@ struct GemmI8 {
 };
 cudaError_t gemm_i8(const GemmI8& g, int kind, bool out_f32, DevError* err, cudaStream_t st, int num_sms);
 int make_tmap_i8(CUtensorMap* m, const void* base, int rows, int cols, long ld, int box_rows);
+int make_tmap_i8_blocks(CUtensorMap* m, const void* base, int rows, int cols, long ld, int box_rows, int blocks);
 int make_tmap_heads(CUtensorMap* m, const void* base, int dims, int tokens, int heads, int batch, long s_token,
                     long s_head, long s_batch);
 
