@@ -129,3 +129,16 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         kb.gemm_int8(x.to(torch.int8), torch.ones(4), x.to(torch.int8), torch.ones(4))
     with pytest.raises(ValueError, match="CUDA"):
         kb.attention_scored(*[torch.zeros(1, 2, 1, 64)] * 3)
+
+
+def test_binding_packs_the_arguments_as_the_c_structure():
+    """The packed bytes of attention_scored are the C structure, field by field."""
+    values = [16 * (i + 1) for i in range(10)] + list(range(100, 112)) + list(range(1, 9)) + [0.5, 30.0]
+    raw = kb._SCORED_PACK(*values)
+    assert len(raw) == ctypes.sizeof(kb.ScoredAttention)
+    a = kb.ScoredAttention.from_buffer_copy(raw)
+    flat = []
+    for name, kind in kb.ScoredAttention._fields_:
+        v = getattr(a, name)
+        flat += list(v) if hasattr(v, "__len__") else [v]
+    assert flat == values

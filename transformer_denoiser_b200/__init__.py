@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -232,75 +233,106 @@ def global_to_local_root(root, x, lengths):
 # ------------------------------------------------------------ 8-bit projections, scored attention
 #
 # These take CUDA tensors of one device, which need not be the current one; work is enqueued
-# on that device's current stream and outputs are allocated there.
+# on that device's current stream and outputs are allocated there.  A call on a single token
+# takes a few microseconds on the GPU, so the checks are written to cost little on the host.
 
-def _same_device(*tensors):
-    """The CUDA device that all given tensors are on."""
-    dev = tensors[0].device
-    if dev.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device")
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors are on different devices ({dev} and {t.device})")
+_SCORED_PACK = struct.Struct("10Q12q8i2f").pack   # struct kimodo_scored_attention
+_T = None            # torch, once it is needed
+_raw_stream = None   # device index -> cudaStream_t of its current stream
+_current_device = None
+
+
+def _use_torch():
+    global _T, _raw_stream, _current_device
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda d: torch.cuda.current_stream(d).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _T = torch
+    return torch
+
+
+def _device_of(t, what):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{what} must be a CUDA tensor")
     return dev
 
 
-def _dtype_flag(t, what):
+def _also_on(dev, **tensors):
+    """Raises unless every given tensor is on CUDA device `dev`."""
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev} with the other tensors (it is on {t.device})")
+
+
+def _float_flag(t, what):
     """1 for bf16, 0 for fp32."""
-    import torch
-    if t.dtype == torch.bfloat16:
+    dt = t.dtype
+    if dt is _T.bfloat16:
         return 1
-    if t.dtype == torch.float32:
+    if dt is _T.float32:
         return 0
-    raise ValueError(f"{what} must be bf16 or fp32 (got {t.dtype})")
+    raise ValueError(f"{what} must be bf16 or fp32 (got {dt})")
 
 
-def _need(t, what, dtype, shape=None):
-    """Checks an optional contiguous tensor and returns its data pointer."""
+def _rows_of(t, what):
+    """(rows, columns, row stride) of a 2-D tensor with consecutive columns."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D tensor (got {t.dim()} dimensions)")
+    rows, cols = t.shape
+    ld, sc = t.stride()
+    if sc != 1 and cols > 1:
+        raise ValueError(f"{what} must have a unit column stride")
+    return rows, cols, ld if rows > 1 else cols   # the stride of a single row is never used
+
+
+def _vector(t, what, n):
+    """Data pointer of a contiguous fp32 [n] tensor."""
+    if t.dtype is not _T.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous fp32 tensor of {n} values (got {t.dtype}, {tuple(t.shape)})")
+    return t.data_ptr()
+
+
+def _indices(t, what, shape):
+    """Data pointer of a contiguous int32 tensor, 0 for None."""
     if t is None:
-        return None
-    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} (got {t.dtype}, {tuple(t.shape)})")
+        return 0
+    if t.dtype is not _T.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape} (got {t.dtype}, {tuple(t.shape)})")
     return t.data_ptr()
 
 
 def _launch(dev, fn, *args):
-    """fn(*args, stream) on `dev`'s current stream, with `dev` current."""
-    import torch
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    """fn(*args, stream) on device `dev`'s current stream, with `dev` current."""
+    if dev == _current_device():
+        status = fn(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        with _T.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    if status:
+        _check(status)
 
 
-def _rows_of(x, what):
-    """Row stride of a 2-D tensor with consecutive columns."""
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError(f"{what} must be a 2-D tensor with unit column stride")
-    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
-
-
-def _int8_rows(rows, cols, dev):
-    """An int8 [rows, cols] tensor whose rows start on 16-byte boundaries, as gemm_int8 asks."""
-    import torch
+def _int8_rows(x, rows, cols):
+    """An int8 [rows, cols] tensor on x's device whose rows start on 16-byte boundaries, as gemm_int8 asks."""
     if cols % 16 == 0:
-        return torch.empty((rows, cols), dtype=torch.int8, device=dev)
-    return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=dev)[:, :cols]
+        return x.new_empty((rows, cols), dtype=_T.int8)
+    return x.new_empty((rows, (cols + 15) // 16 * 16), dtype=_T.int8)[:, :cols]
 
 
 def quantize_int8(x):
     """(q, scale) of the rows of x [rows, cols] (fp32 or bf16): int8 [rows, cols] with rows on
     16-byte boundaries and fp32 [rows], x ~ q * scale[:, None]."""
-    import torch
-    lib = load_library()
-    dev = _same_device(x)
-    flag, ldx = _dtype_flag(x, "x"), _rows_of(x, "x")
-    rows, cols = x.shape
-    q = _int8_rows(rows, cols, dev)
-    scale = torch.empty(rows, dtype=torch.float32, device=dev)
-    _launch(dev, lib.kimodo_quantize_int8, x.data_ptr(), ldx, flag, q.data_ptr(), q.stride(0), scale.data_ptr(), rows,
-            cols)
+    lib = _lib or load_library()
+    T = _T or _use_torch()
+    dev = _device_of(x, "x")
+    flag = _float_flag(x, "x")
+    rows, cols, ldx = _rows_of(x, "x")
+    q = _int8_rows(x, rows, cols)
+    scale = x.new_empty(rows, dtype=T.float32)
+    _launch(dev, lib.kimodo_quantize_int8, x.data_ptr(), ldx, flag, q.data_ptr(), (cols + 15) // 16 * 16,
+            scale.data_ptr(), rows, cols)
     return q, scale
 
 
@@ -308,29 +340,33 @@ def rms_norm_int8(x, gamma, residual=None, eps=1e-6, residual_out=None):
     """(q, scale, residual_out): int8 rows and fp32 scales of the RMS norm of x + residual times
     gamma (fp32 [cols]), and the sum in the residual's type (None without a residual).
     x and residual [rows, cols], fp32 or bf16; residual_out may be residual itself."""
-    import torch
-    lib = load_library()
-    dev = _same_device(x, gamma, residual, residual_out)
-    flag, ldx = _dtype_flag(x, "x"), _rows_of(x, "x")
-    rows, cols = x.shape
+    lib = _lib or load_library()
+    T = _T or _use_torch()
+    dev = _device_of(x, "x")
+    flag = _float_flag(x, "x")
+    rows, cols, ldx = _rows_of(x, "x")
     rp = rop = None
     ldr = ldro = rflag = 0
     if residual is not None:
-        if residual.shape != x.shape:
+        rflag = _float_flag(residual, "residual")
+        rr, rc, ldr = _rows_of(residual, "residual")
+        if rr != rows or rc != cols:
             raise ValueError("residual must have the shape of x")
         if residual_out is None:
-            residual_out = torch.empty((rows, cols), dtype=residual.dtype, device=dev)
-        elif residual_out.shape != x.shape or residual_out.dtype != residual.dtype:
-            raise ValueError("residual_out must have the shape and type of residual")
-        rflag, ldr, ldro = _dtype_flag(residual, "residual"), _rows_of(residual, "residual"), _rows_of(residual_out, "residual_out")
+            residual_out = x.new_empty((rows, cols), dtype=residual.dtype)
+            ldro = cols
+        else:
+            rr, rc, ldro = _rows_of(residual_out, "residual_out")
+            if rr != rows or rc != cols or residual_out.dtype is not residual.dtype:
+                raise ValueError("residual_out must have the shape and type of residual")
         rp, rop = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
-    q = _int8_rows(rows, cols, dev)
-    scale = torch.empty(rows, dtype=torch.float32, device=dev)
+    _also_on(dev, gamma=gamma, residual=residual, residual_out=residual_out)
+    q = _int8_rows(x, rows, cols)
+    scale = x.new_empty(rows, dtype=T.float32)
     _launch(dev, lib.kimodo_rms_norm_int8, x.data_ptr(), ldx, flag, rp, ldr, rop, ldro, rflag,
-            _need(gamma, "gamma", torch.float32, (cols,)), float(eps), q.data_ptr(), q.stride(0), scale.data_ptr(), rows,
-            cols)
+            _vector(gamma, "gamma", cols), eps, q.data_ptr(), (cols + 15) // 16 * 16, scale.data_ptr(), rows, cols)
     return q, scale, residual_out
 
 
@@ -338,30 +374,38 @@ def gemm_int8(a, a_scale, w, w_scale, bias=None, epilogue=EPI_BIAS, out_f32=Fals
     """out = epilogue(a_scale[:, None] * w_scale * (a w^T) + bias): int8 a [M, K], w [N, K] (rows on
     16-byte boundaries), fp32 scales [M], [N] and bias [N] or None; out bf16 or fp32 [M, N];
     resid fp32 [M, N] with EPI_BIAS_RESID (may be out)."""
-    import torch
-    lib = load_library()
-    dev = _same_device(a, a_scale, w, w_scale, bias, resid, out)
-    if a.dtype != torch.int8 or w.dtype != torch.int8:
-        raise ValueError("a and w must be int8")
-    lda, ldw = _rows_of(a, "a"), _rows_of(w, "w")
-    (M, K), N = a.shape, w.shape[0]
-    if w.shape[1] != K:
-        raise ValueError(f"a has {K} columns, w {w.shape[1]}")
+    lib = _lib or load_library()
+    T = _T or _use_torch()
+    dev = _device_of(a, "a")
+    if a.dtype is not T.int8 or w.dtype is not T.int8:
+        raise ValueError(f"a and w must be int8 (got {a.dtype}, {w.dtype})")
+    M, K, lda = _rows_of(a, "a")
+    N, K2, ldw = _rows_of(w, "w")
+    if K != K2:
+        raise ValueError(f"a has {K} columns, w {K2}")
     if M == 1:   # the stride of a single row is never used
         lda = (K + 15) // 16 * 16
     if N == 1:
         ldw = (K + 15) // 16 * 16
-    dtype = torch.float32 if out_f32 else torch.bfloat16
+    dtype = T.float32 if out_f32 else T.bfloat16
+    rp = None
+    ldr = 0
+    if resid is not None:
+        rm, rn, ldr = _rows_of(resid, "resid")
+        if resid.dtype is not T.float32 or rm != M or rn != N:
+            raise ValueError(f"resid must be an fp32 tensor of shape {(M, N)}")
+        rp = resid.data_ptr()
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=dev)
-    elif out.dtype != dtype or tuple(out.shape) != (M, N):
-        raise ValueError(f"out must be a {dtype} tensor of shape {(M, N)}")
-    if resid is not None and (resid.dtype != torch.float32 or tuple(resid.shape) != (M, N)):
-        raise ValueError(f"resid must be an fp32 tensor of shape {(M, N)}")
-    _launch(dev, lib.kimodo_gemm_int8, a.data_ptr(), lda, _need(a_scale, "a_scale", torch.float32, (M,)), w.data_ptr(),
-            ldw, _need(w_scale, "w_scale", torch.float32, (N,)), _need(bias, "bias", torch.float32, (N,)),
-            None if resid is None else resid.data_ptr(), 0 if resid is None else _rows_of(resid, "resid"),
-            out.data_ptr(), _rows_of(out, "out"), M, N, K, int(epilogue), int(bool(out_f32)))
+        out = a.new_empty((M, N), dtype=dtype)
+        ldo = N
+    else:
+        om, on, ldo = _rows_of(out, "out")
+        if out.dtype is not dtype or om != M or on != N:
+            raise ValueError(f"out must be a {dtype} tensor of shape {(M, N)}")
+    _also_on(dev, a_scale=a_scale, w=w, w_scale=w_scale, bias=bias, resid=resid, out=out)
+    _launch(dev, lib.kimodo_gemm_int8, a.data_ptr(), lda, _vector(a_scale, "a_scale", M), w.data_ptr(), ldw,
+            _vector(w_scale, "w_scale", N), None if bias is None else _vector(bias, "bias", N), rp, ldr, out.data_ptr(),
+            ldo, M, N, K, epilogue, 1 if out_f32 else 0)
     return out
 
 
@@ -374,38 +418,45 @@ def attention_scored(q, k, v, scale=None, cap=0.0, slopes=None, causal=False, pr
     all; documents int32 [B, Sq], [B, Sk]: only equal numbers >= 0 meet; kv_lengths int32
     [B]; q_start int32 [B]: position of the first query (default Sk - Sq).  A query that sees
     no key gets 0.  Returns [B, Sq, Hq, D]."""
-    import torch
-    lib = load_library()
-    dev = _same_device(q, k, v, slopes, prefix, q_documents, kv_documents, kv_lengths, q_start, out)
-    bf = _dtype_flag(q, "q")
+    lib = _lib or load_library()
+    T = _T or _use_torch()
+    dev = _device_of(q, "q")
+    bf = _float_flag(q, "q")
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be 4-D [batch, tokens, heads, dims]")
-    (B, Sq, Hq, D), (Bk, Sk, Hkv, Dk) = q.shape, k.shape
-    if k.dtype != q.dtype or v.dtype != q.dtype or v.shape != k.shape or Bk != B or Dk != D:
+    B, Sq, Hq, D = q.shape
+    Bk, Sk, Hkv, Dk = k.shape
+    if k.dtype is not q.dtype or v.dtype is not q.dtype or v.shape != k.shape or Bk != B or Dk != D:
         raise ValueError("q, k and v must agree in type, batch and dims, and k and v in shape")
     if out is None:
-        out = torch.empty((B, Sq, Hq, D), dtype=q.dtype, device=dev)
-    elif out.dtype != q.dtype or out.shape != q.shape:
+        out = q.new_empty((B, Sq, Hq, D))
+    elif out.dtype is not q.dtype or out.shape != q.shape:
         raise ValueError("out must have the shape and type of q")
-    strides = []
-    for t, what in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        s = t.stride()
-        if s[3] != 1:
-            raise ValueError(f"the last dimension of {what} must be consecutive")
-        strides.append(s[:3])
-    i32 = torch.int32
-    args = ScoredAttention(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _need(slopes, "slopes", torch.float32, (Hq,)),
-        _need(prefix, "prefix", i32, (B,)), _need(q_documents, "q_documents", i32, (B, Sq)),
-        _need(kv_documents, "kv_documents", i32, (B, Sk)), _need(kv_lengths, "kv_lengths", i32, (B,)),
-        _need(q_start, "q_start", i32, (B,)), *strides, B, Sq, Sk, Hq, Hkv, D, BF16 if bf else FP32, int(bool(causal)),
-        D ** -0.5 if scale is None else float(scale), float(cap))
-    ref = ctypes.byref(args)
+    q0, q1, q2, q3 = q.stride()
+    k0, k1, k2, k3 = k.stride()
+    v0, v1, v2, v3 = v.stride()
+    o0, o1, o2, o3 = out.stride()
+    if q3 != 1 or k3 != 1 or v3 != 1 or o3 != 1:
+        raise ValueError("the last dimension of q, k, v and out must be consecutive")
+    _also_on(dev, k=k, v=v, slopes=slopes, prefix=prefix, q_documents=q_documents, kv_documents=kv_documents,
+             kv_lengths=kv_lengths, q_start=q_start, out=out)
+    args = _SCORED_PACK(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if slopes is None else _vector(slopes, "slopes", Hq),
+        _indices(prefix, "prefix", (B,)), _indices(q_documents, "q_documents", (B, Sq)),
+        _indices(kv_documents, "kv_documents", (B, Sk)), _indices(kv_lengths, "kv_lengths", (B,)),
+        _indices(q_start, "q_start", (B,)), q0, q1, q2, k0, k1, k2, v0, v1, v2, o0, o1, o2, B, Sq, Sk, Hq, Hkv, D, bf,
+        1 if causal else 0, D ** -0.5 if scale is None else scale, cap)
     size = ctypes.c_size_t()
-    with torch.cuda.device(dev):
-        _check(lib.kimodo_attention_scored_workspace(ref, ctypes.byref(size)))
-        ws = torch.empty(size.value, dtype=torch.uint8, device=dev) if size.value else None
-        _launch(dev, lib.kimodo_attention_scored, ref, None if ws is None else ws.data_ptr(), size.value)
+    if dev == _current_device():
+        status = lib.kimodo_attention_scored_workspace(args, ctypes.byref(size))
+    else:
+        with T.cuda.device(dev):
+            status = lib.kimodo_attention_scored_workspace(args, ctypes.byref(size))
+    if status:
+        _check(status)
+    n = size.value
+    ws = q.new_empty(n, dtype=T.uint8) if n else None
+    _launch(dev, lib.kimodo_attention_scored, args, ws.data_ptr() if n else None, n)
     return out
 
 
