@@ -1212,28 +1212,33 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 // ---------------------------------------------------------------- fp32
 //
 // The fp32 path on the FMA units (the tensor cores have no fp32 kind, and tf32 rounds too
-// much).  A CTA of 128 threads takes 16 * TM rows and walks key tiles of 32: thread (row
-// group, column group) holds TM x 4 scores and TM x HD / 8 outputs in registers; keys, values,
-// queries and weights pass through shared memory, rows padded by 16 bytes so that the
-// column groups of a warp read different banks.  A row's statistics live in the 8 lanes that
-// share it.  TM = 4 for many rows, 1 where at most 16 would leave the rest idle.
-constexpr int FT = 32;                       // keys of a tile
-template <int HD, int TM>
+// much).  A CTA takes BM rows and walks key tiles of FT: thread (row group, column group) holds
+// TM x 4 scores and TM x 4 HD / FT outputs in registers.  A 16-byte shared-memory load costs
+// four cycles of the SM's one port whatever its lanes share, in which the FMA units do 16
+// multiplications a lane, so shared memory bounds these tiles (4 rows: 8 loads for 64
+// multiplications of the scores, 12 for 128 of the outputs).  Rows are padded by 16 bytes,
+// so that the eight lanes of a load's phase read different banks; the weights take the keys'
+// place.  A row's statistics live in the lanes that share it.
+// Many rows: 64 rows (256 threads, 4 rows each) by 64 keys; where blocks of 64 would leave over a
+// tenth of the rows idle, 32 rows by 32 keys (32 x 8 heads x 151 tokens, ragged: 137 us
+// against 160; 16 heads x 1000 tokens: 355 against 262); at most 16 rows: 16 by 64.
+template <int HD, int TM, int NT, int FT>
 struct F32Cfg {
-  static constexpr int BM = 16 * TM, LD = HD + 4, LP = FT + 4;
-  static constexpr size_t SMEM = (size_t)(BM * LD + 2 * FT * LD + BM * LP) * 4;
+  static constexpr int CG = FT / 4, RG = NT / CG, BM = RG * TM, LD = HD + 4, LP = FT + 4;
+  static_assert(BM * (FT + 4) <= FT * (HD + 4), "the weights fit in the keys' place");
+  static constexpr size_t SMEM = (size_t)(BM * LD + 2 * FT * LD) * 4;
 };
 
-template <int HD, int TM>
-__global__ void __launch_bounds__(128) scored_f32_kernel(const __grid_constant__ ScoredAttention a,
-                                                         const ScoredPlan plan) {
-  using C = F32Cfg<HD, TM>;
-  constexpr int BM = C::BM, LD = C::LD, LP = C::LP, ND = HD / 32;   // float4 of outputs per row and thread
+template <int HD, int TM, int NT, int FT>
+__global__ void __launch_bounds__(NT, FT == 32 ? 4 : 2) scored_f32_kernel(const __grid_constant__ ScoredAttention a,
+                                                            const __grid_constant__ ScoredPlan plan) {
+  using C = F32Cfg<HD, TM, NT, FT>;
+  constexpr int CG = C::CG, RG = C::RG, BM = C::BM, LD = C::LD, LP = C::LP, ND = HD / (4 * CG);   // float4 of outputs per row and thread
   extern __shared__ float fsm[];
   float* sQ = fsm;
   float* sK = sQ + BM * LD;
+  float* sP = sK;
   float* sV = sK + FT * LD;
-  float* sP = sV + FT * LD;
   ptx::pdl_wait();
   ptx::pdl_trigger();
   long id = blockIdx.x;
@@ -1245,11 +1250,32 @@ __global__ void __launch_bounds__(128) scored_f32_kernel(const __grid_constant__
   const int rb = plan.row_blocks - 1 - (int)(id / a.B);
   const int rows = a.Sq * a.G, row0 = rb * BM;
   const SeqInfo seq = sequence_info(a, b);
-  const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;            // column group, row group (16)
+  const int cg = threadIdx.x % CG, rg = threadIdx.x / CG;
   const int row_end = min(row0 + BM, rows);
 
+  const int key_end = 1 + last_key(a, seq, (long)seq.start + (row_end - 1) / a.G);
+  const int jt_all = (key_end + FT - 1) / FT;
+  const int jt0 = min(split * plan.tiles_per_split, jt_all), jt1 = min(jt0 + plan.tiles_per_split, jt_all);
+  const bool docs = a.q_doc != nullptr;
+  const float* kb = static_cast<const float*>(a.k) + b * a.k_batch + hk * a.k_head;
+  const float* vb = static_cast<const float*>(a.v) + b * a.v_batch + hk * a.v_head;
+  // one tile's rows into shared memory, those past the last key as zeros
+  auto fetch = [&](float* dst, const float* src, long stride, int j0) {
+    const uint32_t d0 = ptx::smem_u32(dst);
+#pragma unroll 4
+    for (int c = threadIdx.x; c < FT * (HD / 4); c += NT) {
+      const int lj = c / (HD / 4), ch = c % (HD / 4), j = j0 + lj;
+      const bool in = j < seq.kv_len;
+      ptx::cp_async_16_zfill(d0 + (uint32_t)(lj * LD + ch * 4) * 4, src + (in ? j : 0) * stride + ch * 4, in);
+    }
+    ptx::cp_async_commit();
+  };
+  if (jt0 < jt1) {
+    fetch(sK, kb, a.k_token, jt0 * FT);
+    fetch(sV, vb, a.v_token, jt0 * FT);
+  }
   const float* qb = static_cast<const float*>(a.q) + b * a.q_batch + (long)hk * a.G * a.q_head;
-  for (int c = threadIdx.x; c < BM * (HD / 4); c += 128) {
+  for (int c = threadIdx.x; c < BM * (HD / 4); c += NT) {
     const int lr = c / (HD / 4), ch = c % (HD / 4), r = row0 + lr;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < rows) {
@@ -1258,13 +1284,13 @@ __global__ void __launch_bounds__(128) scored_f32_kernel(const __grid_constant__
     }
     *reinterpret_cast<float4*>(sQ + lr * LD + ch * 4) = v;
   }
-  // row u of this thread: local row rg + 16 u (so that a warp's four rows differ in banks)
+  // row u of this thread: local row rg + 8 u
   int last[TM], pos[TM], doc[TM];
   float slope[TM], m[TM], l[TM];
   float4 o[TM][ND];
 #pragma unroll
   for (int u = 0; u < TM; ++u) {
-    const int r = row0 + rg + 16 * u;
+    const int r = row0 + rg + RG * u;
     const bool ok = r < rows;
     const int i = ok ? r / a.G : 0, g = ok ? r - i * a.G : 0;
     pos[u] = seq.start + i;
@@ -1276,63 +1302,51 @@ __global__ void __launch_bounds__(128) scored_f32_kernel(const __grid_constant__
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[u][d] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const int key_end = 1 + last_key(a, seq, (long)seq.start + (row_end - 1) / a.G);
-  const int jt_all = (key_end + FT - 1) / FT;
-  const int jt0 = min(split * plan.tiles_per_split, jt_all), jt1 = min(jt0 + plan.tiles_per_split, jt_all);
-  const bool docs = a.q_doc != nullptr;
-  const float* kb = static_cast<const float*>(a.k) + b * a.k_batch + hk * a.k_head;
-  const float* vb = static_cast<const float*>(a.v) + b * a.v_batch + hk * a.v_head;
   for (int jt = jt0; jt < jt1; ++jt) {
     const int j0 = jt * FT;
+    asm volatile("cp.async.wait_group 1;" ::: "memory");   // the keys
     __syncthreads();
-    for (int c = threadIdx.x; c < FT * (HD / 4); c += 128) {
-      const int lj = c / (HD / 4), ch = c % (HD / 4), j = j0 + lj;
-      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-      if (j < seq.kv_len) {
-        kv = *reinterpret_cast<const float4*>(kb + j * a.k_token + ch * 4);
-        vv = *reinterpret_cast<const float4*>(vb + j * a.v_token + ch * 4);
-      }
-      *reinterpret_cast<float4*>(sK + lj * LD + ch * 4) = kv;
-      *reinterpret_cast<float4*>(sV + lj * LD + ch * 4) = vv;
-    }
-    __syncthreads();
-    // scores of keys cg + 8 w
+    // scores of keys cg + 16 w, two key halves of the products a register pair
     float2 acc[TM][4];
 #pragma unroll
     for (int u = 0; u < TM; ++u)
 #pragma unroll
       for (int w = 0; w < 4; ++w) acc[u][w] = make_float2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 2
     for (int d = 0; d < HD; d += 4) {
-      float4 q4[TM], k4[4];
+      float4 k4[4];
 #pragma unroll
-      for (int u = 0; u < TM; ++u) q4[u] = *reinterpret_cast<const float4*>(sQ + (rg + 16 * u) * LD + d);
+      for (int w = 0; w < 4; ++w) k4[w] = *reinterpret_cast<const float4*>(sK + (cg + CG * w) * LD + d);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) k4[w] = *reinterpret_cast<const float4*>(sK + (cg + 8 * w) * LD + d);
-#pragma unroll
-      for (int u = 0; u < TM; ++u)
+      for (int u = 0; u < TM; ++u) {
+        const float4 q4 = *reinterpret_cast<const float4*>(sQ + (rg + RG * u) * LD + d);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          acc[u][w] = __ffma2_rn(make_float2(q4[u].x, q4[u].y), make_float2(k4[w].x, k4[w].y), acc[u][w]);
-          acc[u][w] = __ffma2_rn(make_float2(q4[u].z, q4[u].w), make_float2(k4[w].z, k4[w].w), acc[u][w]);
+          acc[u][w] = __ffma2_rn(make_float2(q4.x, q4.y), make_float2(k4[w].x, k4[w].y), acc[u][w]);
+          acc[u][w] = __ffma2_rn(make_float2(q4.z, q4.w), make_float2(k4[w].z, k4[w].w), acc[u][w]);
         }
+      }
     }
+    int kd[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      kd[w] = docs && j0 + cg + CG * w < a.Sk ? a.kv_doc[(long)b * a.Sk + j0 + cg + CG * w] : -1;
+    __syncthreads();   // all have read the keys: the weights take their place
 #pragma unroll
     for (int u = 0; u < TM; ++u) {
       float x[4], top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const int j = j0 + cg + 8 * w;
+        const int j = j0 + cg + CG * w;
         float y = (acc[u][w].x + acc[u][w].y) * a.scale;
         y = a.cap > 0.f ? a.cap * tanhf(y / a.cap) * LOG2E : y * LOG2E;
         if (a.slopes) y = fmaf(-slope[u], fabsf((float)(pos[u] - j)), y);
-        bool seen = j <= last[u];
-        if (docs && seen) seen = doc[u] >= 0 && a.kv_doc[(long)b * a.Sk + j] == doc[u];
+        const bool seen = j <= last[u] && (!docs || (doc[u] >= 0 && kd[w] == doc[u]));
         x[w] = seen ? y : -INFINITY;
         top = fmaxf(top, x[w]);
       }
 #pragma unroll
-      for (int s = 1; s < 8; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      for (int s = 1; s < CG; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
       const float mn = fmaxf(m[u], top), ref = mn == -INFINITY ? 0.f : mn;
       const float f = exp2f(m[u] - ref);
       m[u] = mn;
@@ -1341,7 +1355,7 @@ __global__ void __launch_bounds__(128) scored_f32_kernel(const __grid_constant__
       for (int w = 0; w < 4; ++w) {
         const float p = exp2f(x[w] - ref);
         sum += p;
-        sP[(rg + 16 * u) * LP + cg + 8 * w] = p;
+        sP[(rg + RG * u) * LP + cg + CG * w] = p;
       }
       l[u] = l[u] * f + sum;
 #pragma unroll
@@ -1349,36 +1363,46 @@ __global__ void __launch_bounds__(128) scored_f32_kernel(const __grid_constant__
         o[u][d].x *= f; o[u][d].y *= f; o[u][d].z *= f; o[u][d].w *= f;
       }
     }
-    __syncwarp();   // a row's weights are read by the 8 lanes that wrote them
-    // outputs: dims 4 cg + 32 d
-#pragma unroll 2
+    asm volatile("cp.async.wait_group 0;" ::: "memory");   // the values
+    __syncthreads();
+    // outputs: dims 4 cg + 64 d
+#pragma unroll 1
     for (int j = 0; j < FT; j += 4) {
-      float4 p4[TM];
-#pragma unroll
-      for (int u = 0; u < TM; ++u) p4[u] = *reinterpret_cast<const float4*>(sP + (rg + 16 * u) * LP + j);
+      float4 v4[4][ND];
 #pragma unroll
       for (int w = 0; w < 4; ++w)
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          const float4 v = *reinterpret_cast<const float4*>(sV + (j + w) * LD + 32 * d + 4 * cg);
+        for (int d = 0; d < ND; ++d) v4[w][d] = *reinterpret_cast<const float4*>(sV + (j + w) * LD + 4 * CG * d + 4 * cg);
 #pragma unroll
-          for (int u = 0; u < TM; ++u) {
-            const float p = w == 0 ? p4[u].x : w == 1 ? p4[u].y : w == 2 ? p4[u].z : p4[u].w;
-            float2 lo = __ffma2_rn(make_float2(p, p), make_float2(v.x, v.y), make_float2(o[u][d].x, o[u][d].y));
-            float2 hi = __ffma2_rn(make_float2(p, p), make_float2(v.z, v.w), make_float2(o[u][d].z, o[u][d].w));
+      for (int u = 0; u < TM; ++u) {
+        const float4 p4 = *reinterpret_cast<const float4*>(sP + (rg + RG * u) * LP + j);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float p = w == 0 ? p4.x : w == 1 ? p4.y : w == 2 ? p4.z : p4.w;
+          const float2 pp = make_float2(p, p);
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const float2 lo = __ffma2_rn(pp, make_float2(v4[w][d].x, v4[w][d].y), make_float2(o[u][d].x, o[u][d].y));
+            const float2 hi = __ffma2_rn(pp, make_float2(v4[w][d].z, v4[w][d].w), make_float2(o[u][d].z, o[u][d].w));
             o[u][d] = make_float4(lo.x, lo.y, hi.x, hi.y);
           }
         }
+      }
+    }
+    __syncthreads();   // all have read weights and values: the next tile may come
+    if (jt + 1 < jt1) {
+      fetch(sK, kb, a.k_token, j0 + FT);
+      fetch(sV, vb, a.v_token, j0 + FT);
     }
   }
   const long n_rows = (long)a.B * a.Hkv * rows, prow = ((long)b * a.Hkv + hk) * rows;
 #pragma unroll
   for (int u = 0; u < TM; ++u) {
-    const int r = row0 + rg + 16 * u;
+    const int r = row0 + rg + RG * u;
     const bool row_ok = r < rows;
     float sum = l[u];
 #pragma unroll
-    for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    for (int s = 1; s < CG; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
     const bool seen = sum != 0.f;
     const int i = row_ok ? r / a.G : 0, g = row_ok ? r - i * a.G : 0;
     bool finite = true;
@@ -1390,16 +1414,16 @@ __global__ void __launch_bounds__(128) scored_f32_kernel(const __grid_constant__
       if (row_ok) {
         if (plan.parts == 1)
           *reinterpret_cast<float4*>(static_cast<float*>(a.out) + b * a.o_batch + i * a.o_token +
-                                     (long)(hk * a.G + g) * a.o_head + 32 * d + 4 * cg) = y;
+                                     (long)(hk * a.G + g) * a.o_head + 4 * CG * d + 4 * cg) = y;
         else if (seen)
-          *reinterpret_cast<float4*>(plan.part_o + ((long)split * n_rows + prow + r) * HD + 32 * d + 4 * cg) = y;
+          *reinterpret_cast<float4*>(plan.part_o + ((long)split * n_rows + prow + r) * HD + 4 * CG * d + 4 * cg) = y;
       }
     }
     if (plan.parts == 1) {
       unsigned redo = __ballot_sync(0xffffffffu, row_ok && !finite);
       while (redo) {
         const int src = __ffs(redo) - 1;
-        redo &= ~(0xffu << (src & ~7));     // the 8 lanes of that row
+        redo &= ~(((1u << CG) - 1u) << (src / CG * CG));   // the lanes of that row
         row_by_warp<float, HD>(a, b, hk * a.G + __shfl_sync(0xffffffffu, g, src), __shfl_sync(0xffffffffu, i, src));
       }
     } else if (row_ok && cg == 0) {
@@ -1512,15 +1536,15 @@ cudaError_t run_tc(const ScoredAttention& a, const ScoredPlan& plan, DevError* e
   return e != cudaSuccess ? e : join<bf16, HD>(a, plan, st);
 }
 
-template <int HD, int TM>
+template <int HD, int TM, int NT, int FT>
 cudaError_t launch_f32(const ScoredAttention& a, const ScoredPlan& plan, cudaStream_t st) {
-  using C = F32Cfg<HD, TM>;
-  auto kern = scored_f32_kernel<HD, TM>;
+  using C = F32Cfg<HD, TM, NT, FT>;
+  auto kern = scored_f32_kernel<HD, TM, NT, FT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return e;
   const long grid = (long)plan.row_blocks * a.Hkv * a.B * plan.splits;
   if (grid > INT_MAX) return cudaErrorInvalidValue;
-  e = launch_kernel(kern, dim3((unsigned)grid), dim3(128), C::SMEM, st, a, plan);
+  e = launch_kernel(kern, dim3((unsigned)grid), dim3(NT), C::SMEM, st, a, plan);
   return e != cudaSuccess ? e : join<float, HD>(a, plan, st);
 }
 
@@ -1540,11 +1564,12 @@ ScoredPlan scored_attention_plan(const ScoredAttention& a, bool is_bf16, int num
     fill = p.few ? 4 : 1;
     least = 2;
   } else {
-    p.few = rows <= 16 ? 16 : 0;
-    block = p.few ? 16 : 64;
-    tile = FT;
-    fill = 3;
-    least = 4;
+    const long r64 = (rows + 63) / 64 * 64, r32 = (rows + 31) / 32 * 32;
+    p.few = rows <= 16 ? 16 : r64 * 10 > r32 * 11 ? 32 : 64;
+    block = p.few;
+    tile = p.few == 32 ? 32 : 64;
+    fill = 2;
+    least = 2;
   }
   p.k = scored_const(a.scale, a.cap);
   p.row_blocks = (int)((rows + block - 1) / block);
@@ -1568,9 +1593,9 @@ cudaError_t attention_scored(const ScoredAttention& a, bool is_bf16, ScoredPlan 
     plan.part_lse = plan.part_o + (size_t)plan.parts * a.B * a.Hq * a.Sq * a.HD;
   }
   if (is_bf16) return a.HD == 64 ? run_tc<64>(a, plan, err, st) : run_tc<128>(a, plan, err, st);
-  if (plan.few)
-    return a.HD == 64 ? launch_f32<64, 1>(a, plan, st) : launch_f32<128, 1>(a, plan, st);
-  return a.HD == 64 ? launch_f32<64, 4>(a, plan, st) : launch_f32<128, 4>(a, plan, st);
+  if (plan.few == 16) return a.HD == 64 ? launch_f32<64, 2, 128, 64>(a, plan, st) : launch_f32<128, 2, 128, 64>(a, plan, st);
+  if (plan.few == 32) return a.HD == 64 ? launch_f32<64, 2, 128, 32>(a, plan, st) : launch_f32<128, 2, 128, 32>(a, plan, st);
+  return a.HD == 64 ? launch_f32<64, 4, 256, 64>(a, plan, st) : launch_f32<128, 4, 256, 64>(a, plan, st);
 }
 
 }  // namespace kd

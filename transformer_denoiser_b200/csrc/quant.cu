@@ -86,7 +86,7 @@ __device__ __forceinline__ void row_reduce(float& s, uint32_t& m, float* xs, uin
 }
 
 template <typename TX, typename TR, bool NORM, int TPR, int NG, bool VEC>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rows_int8_kernel(RowsInt8 a) {
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, NORM && TPR == 256 ? 5 : NORM && TPR == 64 ? 20 : 1) rows_int8_kernel(RowsInt8 a) {
   constexpr bool RES = Elem<TR>::size != 0;
   __shared__ float xs[TPR / 32];
   __shared__ uint32_t xm[TPR / 32];
@@ -239,9 +239,19 @@ cudaError_t run_rows(const RowsInt8& a, cudaStream_t st) {
                : launch_kernel(rows_int8_kernel<TX, TR, NORM, TPR_, NG_, false>, dim3((unsigned)grid),      \
                                dim3(block), 0, st, a);                                                      \
   }
-  KD_ROWS(32, 4)
-  KD_ROWS(128, 4)
-  KD_ROWS(512, 4)
+  // The quantisation alone runs best with a row in one warp or few (38528 x 1024 bf16: 19.6 us with
+  // 32 threads a row, 40 with 64 or 128); the norm, which holds gamma and reads the residual too,
+  // with fewer values a thread (38528 x 1024: 67.8 us with 64 threads, 86.8 with 32;
+  // 8192 x 4096: 53 us with 256, 59 with 128).
+  if constexpr (NORM) {
+    KD_ROWS(64, 2)
+    KD_ROWS(256, 2)
+    KD_ROWS(1024, 2)
+  } else {
+    KD_ROWS(32, 4)
+    KD_ROWS(128, 4)
+    KD_ROWS(512, 4)
+  }
   KD_ROWS(1024, 4)
 #undef KD_ROWS
   return cudaErrorInvalidValue;
