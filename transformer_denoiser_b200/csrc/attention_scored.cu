@@ -50,7 +50,7 @@ namespace {
 constexpr int TILE = 128;                    // query rows of a tile, keys of a tile
 constexpr int NUM_THREADS = 640;
 constexpr int STAGES = 4;                    // K and V tiles in flight, alternating
-constexpr int MAX_FLAGS = 8192;              // key tiles whose document ranges a CTA keeps
+constexpr int MAX_LIST = 4096;               // key tiles that a CTA with documents lists (12 bits of an entry)
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr int KIMODO_ETIMEOUT_CODE = -5;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -218,7 +218,7 @@ struct Cfg {
   static constexpr uint32_t HALF = TILE * 128;             // 64 dims of a tile
   // HD 64 would let two CTAs share an SM, whose TMEM holds one: the size keeps them apart
   static constexpr size_t BODY = 2 * Q_BYTES + (size_t)STAGES * KV_BYTES;
-  static constexpr size_t SMEM = 1024 + (BODY < 119808 ? 119808 : BODY) + MAX_FLAGS + 256 + 16 * 64 * 4 + 2 * 2 * 2 * TILE * 4;
+  static constexpr size_t SMEM = 1024 + (BODY < 119808 ? 119808 : BODY) + MAX_LIST * 2 + 256 + 16 * 64 * 4 + 2 * 2 * 2 * TILE * 4;
 };
 constexpr uint32_t TMEM_COLS = 512;
 __device__ __forceinline__ uint32_t s_col(int t) { return 128u * t; }
@@ -252,8 +252,8 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = ptx::smem_u32(smem);
   const uint32_t sKV = sQ + 2 * C::Q_BYTES;
-  uint8_t* flags = smem + C::BODY;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(flags + MAX_FLAGS);
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::BODY);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(list + MAX_LIST);
   const uint32_t bar0 = ptx::smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
@@ -263,8 +263,9 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 6);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* mma_lock = reinterpret_cast<int*>(tmem_slot + 2);
+  int* list_len = mma_lock + 1;
   RowTile* tiles = reinterpret_cast<RowTile*>(tmem_slot + 4);
-  int* docs_smem = reinterpret_cast<int*>(smem + C::BODY + MAX_FLAGS + 256);   // [16 warps][64]
+  int* docs_smem = reinterpret_cast<int*>(smem + C::BODY + MAX_LIST * 2 + 256);   // [16 warps][64]
   float* xch = reinterpret_cast<float*>(docs_smem + 16 * 64);                  // [2 turns][2 tiles][2 halves][TILE]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -314,16 +315,13 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const int total = 2 * TILE * CH;
     for (int c = threadIdx.x; c < total; c += NUM_THREADS) {
       const int lr = c / CH, ch = c % CH, r = row0 + lr;
-      uint4 val = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows) {
-        const int i = r / a.G, g = r - i * a.G;
-        val = *reinterpret_cast<const uint4*>(qb + i * a.q_token + g * a.q_head + ch * 8);
-      }
+      const bool in = r < rows;
+      const int i = in ? r / a.G : 0, g = in ? r - i * a.G : 0;
       const int t = lr / TILE, rr = lr % TILE;
-      *reinterpret_cast<uint4*>(smem + t * C::Q_BYTES + (ch >> 3) * C::HALF + rr * 128 +
-                                (((ch & 7) ^ (rr & 7)) << 4)) = val;
+      ptx::cp_async_16_zfill(sQ + t * C::Q_BYTES + (ch >> 3) * C::HALF + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+                             qb + i * a.q_token + g * a.q_head + ch * 8, in);
     }
-    ptx::fence_proxy_async_smem();
+    ptx::cp_async_commit();   // waited for below, under the key tiles' documents
   }
   // this softmax thread's row
   const int t_own = warp >= 12 ? 1 : 0;
@@ -353,10 +351,10 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const int jt0 = min(split * plan.tiles_per_split, jt_all);
   const int jt1 = plan.splits == 1 ? jt_all : min(jt0 + plan.tiles_per_split, jt_all);
   const bool docs = a.q_doc != nullptr;
-  const bool listed = docs && jt1 - jt0 <= MAX_FLAGS;
+  const bool listed = docs && jt1 - jt0 <= MAX_LIST;
   if (listed) {
-    // flags of a key tile: bit 2t = row tile t may see it, bit 2t + 1 = all of t's rows and all
-    // of its keys are one document
+    // entry of a key tile: its number above 4 flags, bit 2t = row tile t may see it, bit 2t + 1 =
+    // all of t's rows and all of its keys are one document
     constexpr int AT_ONCE = 4;   // tiles whose loads a warp has in flight
     for (int jq = jt0 + warp; jq < jt1; jq += AT_ONCE * (NUM_THREADS / 32)) {
       int d[AT_ONCE][TILE / 32];
@@ -388,11 +386,25 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             if (lo <= q.docs_hi && q.docs_lo <= hi) f |= 1u << (2 * t);
             if (!none && !q.any_none && lo == hi && q.docs_lo == q.docs_hi && lo == q.docs_lo) f |= 2u << (2 * t);
           }
-          flags[jt - jt0] = f;
+          list[jt - jt0] = (uint16_t)((jt - jt0) << 4 | f);
         }
       }
     }
+    __syncthreads();
+    if (warp == 0) {   // close the gaps: the tiles that neither row tile sees
+      int len = 0;
+      for (int e = 0; e < jt1 - jt0; e += 32) {
+        const uint32_t v = e + lane < jt1 - jt0 ? list[e + lane] : 0u;
+        const unsigned keep = __ballot_sync(0xffffffffu, v & 5u);
+        if (v & 5u) list[len + __popc(keep & ((1u << lane) - 1u))] = (uint16_t)v;
+        len += __popc(keep);
+        __syncwarp();
+      }
+      if (lane == 0) *list_len = len;
+    }
   }
+  ptx::cp_async_wait_all();
+  ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -406,9 +418,10 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     return min((1 + last_key(a, seq, (long)seq.start + r_b / a.G) + TILE - 1) / TILE, jt1);
   };
   const int end0 = end_of(0), end1 = end_of(1);
-  auto takes = [&](int t, int jt) -> bool {
-    return jt < (t ? end1 : end0) && (!listed || ((flags[jt - jt0] >> (2 * t)) & 1));
-  };
+  const int n_tiles = listed ? *list_len : jt1 - jt0;
+  // entry n of the tiles to go through: key tile and the flags above
+  auto entry = [&](int n) -> int { return listed ? list[n] : n << 4 | (docs ? 5 : 15); };
+  auto takes = [&](int t, int e) -> bool { return jt0 + (e >> 4) < (t ? end1 : end0) && ((e >> (2 * t)) & 1); };
 
   // registers: 640 x 96 at launch cover 128 x 64 + 512 x 104
   if (warp < 4) {
@@ -420,8 +433,9 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         uint32_t phase = 0;
         long issued = 0;
         bool ok = true;
-        for (int jt = jt0; jt < jt1 && ok; ++jt) {
-          if (!takes(0, jt) && !takes(1, jt)) continue;
+        for (int n = 0; n < n_tiles && ok; ++n) {
+          const int e = entry(n), jt = jt0 + (e >> 4);
+          if (!takes(0, e) && !takes(1, e)) continue;
           for (int kv = 0; kv < 2; ++kv) {
             if (!ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort, WAIT_LIMIT_NS)) {
               ok = false;
@@ -438,9 +452,9 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         if (!ok && !*abort) record_timeout(err, abort);
         // every copy issued has landed before the CTA leaves (also after a wait that ran out)
-        const long n = issued < STAGES ? issued : STAGES;
+        const long left = issued < STAGES ? issued : STAGES;
         volatile int never = 0;
-        for (long i = 0; i < n; ++i) {
+        for (long i = 0; i < left; ++i) {
           if (--stage < 0) { stage = STAGES - 1; phase ^= 1u; }
           ptx::mbar_wait_bounded(full_bar(stage), phase, &never, WAIT_LIMIT_NS);
         }
@@ -512,9 +526,9 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         __syncwarp();
         if (lane == 0) atomicExch(mma_lock, 0);
       };
-      for (int jt = jt0; jt < jt1; ++jt) {
-        const bool mine = __shfl_sync(0xffffffffu, (int)takes(t, jt), 0) != 0;
-        const bool other = __shfl_sync(0xffffffffu, (int)takes(t ^ 1, jt), 0) != 0;
+      for (int n = 0; n < n_tiles; ++n) {
+        const int e = __shfl_sync(0xffffffffu, entry(n), 0), jt = jt0 + (e >> 4);
+        const bool mine = takes(t, e), other = takes(t ^ 1, e);
         if (!mine && !other) continue;
         const int k_stage = stage;
         const uint32_t k_phase = phase;
@@ -594,11 +608,11 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     float2 l2 = make_float2(0.f, 0.f);   // their sum over this thread's keys
     uint32_t phase = 0;
     bool ok = true, started = false;
-    const int end_t = t ? end1 : end0;
-    for (int jt = jt0; jt < end_t; ++jt) {
-      if (listed && !((flags[jt - jt0] >> (2 * t)) & 1)) continue;
+    for (int n = 0; n < n_tiles; ++n) {
+      const int e = entry(n), jt = jt0 + (e >> 4);
+      if (!takes(t, e)) continue;
       const int j0 = jt * TILE + half * KH;
-      const bool one_doc = !docs || (listed && ((flags[jt - jt0] >> (2 * t + 1)) & 1));
+      const bool one_doc = (e >> (2 * t + 1)) & 1;
       if (!one_doc) {   // the documents of these keys, staged before the scores are there
         dbuf[lane] = kdocs[min(j0 + lane, a.Sk - 1)];
         dbuf[32 + lane] = kdocs[min(j0 + 32 + lane, a.Sk - 1)];
