@@ -47,26 +47,38 @@ __device__ __forceinline__ void record_timeout(DevError* err, int where, volatil
   }
 }
 
-// Residual of channel n for the tokens m0 .. m0 + NV - 1, loaded before the accumulators are there.
+// What a chunk of NV tokens from m0 needs besides its accumulators, loaded a chunk ahead: lane l's
+// token scale and, with a residual, channel n of every token.
 template <int KIND, int NV>
-__device__ __forceinline__ void load_resid(const I8Epi& e, int n, int m0, float (&r)[NV]) {
-  if constexpr (KIND == EPI_BIAS_RESID) {
+struct Ahead {
+  float scale;
+  float resid[KIND == EPI_BIAS_RESID ? NV : 1];
+  __device__ __forceinline__ void load(const I8Epi& e, int n, int m0, int lane) {
+    scale = lane < NV && m0 + lane < e.M ? e.a_scale[m0 + lane] : 0.f;
+    if constexpr (KIND == EPI_BIAS_RESID) {
+      const float* r = e.resid + (long)m0 * e.ldr + n;
+      if (n < e.N && m0 + NV <= e.M) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) r[j] = n < e.N && m0 + j < e.M ? e.resid[(long)(m0 + j) * e.ldr + n] : 0.f;
+        for (int j = 0; j < NV; ++j) resid[j] = r[j * e.ldr];
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) resid[j] = n < e.N && m0 + j < e.M ? r[j * e.ldr] : 0.f;
+      }
+    }
   }
-}
+};
 
 // Finish and store the accumulators v (32-bit integers) of channel n for the tokens
-// m0 .. m0 + NV - 1; sm: lane l holds the scale of token m0 + l.
+// m0 .. m0 + NV - 1.
 template <int KIND, typename OutT, int NV>
-__device__ __forceinline__ void store_tokens(const I8Epi& e, int n, float sn, float bn, int m0, float sm,
-                                             const int (&v)[NV], const float (&r)[NV]) {
+__device__ __forceinline__ void store_tokens(const I8Epi& e, int n, float sn, float bn, int m0,
+                                             const Ahead<KIND, NV>& ahead, const int (&v)[NV]) {
   const bool col = n < e.N;
   float y[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    y[j] = fmaf((float)v[j], __shfl_sync(0xffffffffu, sm, j) * sn, bn);
-    if constexpr (KIND == EPI_BIAS_RESID) y[j] += r[j];
+    y[j] = fmaf((float)v[j], __shfl_sync(0xffffffffu, ahead.scale, j) * sn, bn);
+    if constexpr (KIND == EPI_BIAS_RESID) y[j] += ahead.resid[j];
   }
   if constexpr (KIND == EPI_BIAS_GELU) {
 #pragma unroll
@@ -77,9 +89,18 @@ __device__ __forceinline__ void store_tokens(const I8Epi& e, int n, float sn, fl
     for (int j = 0; j < NV; ++j) y[j] = silu_f(y[j]);
   }
   OutT* o = static_cast<OutT*>(e.out) + (long)m0 * e.ldo + n;
+  if (!col) return;
+  if (m0 + NV <= e.M) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (col && m0 + j < e.M) o[(long)j * e.ldo] = from_f<OutT>(y[j]);
+    for (int j = 0; j < NV; ++j) {
+      *o = from_f<OutT>(y[j]);
+      o += e.ldo;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (m0 + j < e.M) o[j * e.ldo] = from_f<OutT>(y[j]);
+  }
 }
 
 // ====================================================================== CTA pairs (many tokens)
@@ -269,9 +290,9 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
       const int n = w * 256 + (int)rank * 128 + quarter * 32 + lane;
       const float sn = n < ep.N ? ep.w_scale[n] : 0.f;
       const float bn = n < ep.N && ep.bias != nullptr ? ep.bias[n] : 0.f;
-      // 32-token chunks part, part + 2, ...; the residual of a chunk is loaded a chunk ahead
-      float res[32];
-      load_resid<KIND>(ep, n, t * BN + part * 32, res);
+      // 32-token chunks part, part + 2, ...
+      Ahead<KIND, 32> next;
+      next.load(ep, n, t * BN + part * 32, lane);
       if (!ptx::mbar_wait_bounded(tfull_bar(acc), (local >> 1) & 1, abort, WAIT_LIMIT_NS)) {
         if (!*abort) record_timeout(err, WHERE_GEMM_EPILOGUE, abort);
         break;
@@ -282,17 +303,15 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
       for (int c = part * 32; c < BN; c += 64) {
         const int m0 = t * BN + c;
         if (m0 >= ep.M) break;
-        const float sm = m0 + lane < ep.M ? ep.a_scale[m0 + lane] : 0.f;
-        float f[32], now[32];
+        float f[32];
         int v[32];
         ptx::tmem_ld(taddr + c, f);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) now[j] = res[j];
-        if (c + 64 < BN) load_resid<KIND>(ep, n, m0 + 64, res);
+        const Ahead<KIND, 32> now = next;
+        if (c + 64 < BN) next.load(ep, n, m0 + 64, lane);
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __float_as_int(f[j]);
-        store_tokens<KIND, OutT, 32>(ep, n, sn, bn, m0, sm, v, now);
+        store_tokens<KIND, OutT, 32>(ep, n, sn, bn, m0, now, v);
       }
       ptx::tc_fence_before();
       __syncwarp();
@@ -455,10 +474,9 @@ gemm_i8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
       const int n = row < p.ct ? n0 + row : ep.N;   // ep.N: no channel
       const float sn = n < ep.N ? ep.w_scale[n] : 0.f;
       const float bn = n < ep.N && ep.bias != nullptr ? ep.bias[n] : 0.f;
-      constexpr int CH = BN % 32 == 0 ? 32 : 16;   // tokens of a chunk; its residual is loaded a chunk ahead
-      float res[CH];
-      load_resid<KIND>(ep, n, t0, res);
-      const float sm0 = lane < CH && t0 + lane < ep.M ? ep.a_scale[t0 + lane] : 0.f;
+      constexpr int CH = BN % 32 == 0 ? 32 : 16;   // tokens of a chunk
+      Ahead<KIND, CH> next;
+      next.load(ep, n, t0, lane);
       const bool ok = ptx::mbar_wait_bounded(done_bar, 0, abort, WAIT_LIMIT_NS);
       if (!ok && !*abort) record_timeout(err, WHERE_GEMM_EPILOGUE, abort);
       ptx::tc_fence_after();
@@ -468,17 +486,15 @@ gemm_i8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
         for (int c = 0; c < BN; c += CH) {
           const int m0 = t0 + c;
           if (m0 >= ep.M) break;
-          const float sm = c == 0 ? sm0 : lane < CH && m0 + lane < ep.M ? ep.a_scale[m0 + lane] : 0.f;
-          float f[CH], now[CH];
+          float f[CH];
           int v[CH];
           ptx::tmem_ld(taddr + c, f);
-#pragma unroll
-          for (int j = 0; j < CH; ++j) now[j] = res[j];
-          if (c + CH < BN) load_resid<KIND>(ep, n, m0 + CH, res);
+          const Ahead<KIND, CH> now = next;
+          if (c + CH < BN) next.load(ep, n, m0 + CH, lane);
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < CH; ++j) v[j] = __float_as_int(f[j]);
-          store_tokens<KIND, OutT, CH>(ep, n, sn, bn, m0, sm, v, now);
+          store_tokens<KIND, OutT, CH>(ep, n, sn, bn, m0, now, v);
         }
       }
     }
