@@ -598,6 +598,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const bool warp_rows = (warp & 3) * 32 + row0 + t * TILE < rows;
     const int p = seq.start + i_own;
     const int last = row_ok ? last_key(a, seq, (long)seq.start + i_own) : -1;
+    qdoc = qdoc < 0 ? -2 : qdoc;
     const float slope2 = BIAS && row_ok ? a.slopes[hk * a.G + g_own] * LOG2E : 0.f;
     // the constants are those of |scale|: the products take its sign, and a scale of 0 is products of 0
     const ScoredConst& cc = plan.k;
@@ -614,8 +615,9 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       const int j0 = jt * TILE + half * KH;
       const bool one_doc = (e >> (2 * t + 1)) & 1;
       if (!one_doc) {   // the documents of these keys, staged before the scores are there
-        dbuf[lane] = kdocs[min(j0 + lane, a.Sk - 1)];
-        dbuf[32 + lane] = kdocs[min(j0 + 32 + lane, a.Sk - 1)];
+        // (a key in no document: -1, which no row has; a row in none: -2, below)
+        dbuf[lane] = max(kdocs[min(j0 + lane, a.Sk - 1)], -1);
+        dbuf[32 + lane] = max(kdocs[min(j0 + 32 + lane, a.Sk - 1)], -1);
         __syncwarp();
       }
       // after a wait that ran out the rest is gone through without waiting, so that the
@@ -650,7 +652,8 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           return sum;
         };
         // both warps of the rows decide alike: the conditions are those of the rows
-        const bool masked = !one_doc || !__all_sync(0xffffffffu, jt * TILE + TILE - 1 <= last || !row_ok);
+        const bool cut = !__all_sync(0xffffffffu, jt * TILE + TILE - 1 <= last || !row_ok);
+        const bool masked = cut || !one_doc;
         bool done = false, tried = false;
         if (!masked && __all_sync(0xffffffffu, m > -INFINITY || !row_ok)) {
           const float2 nref2 = make_float2(-m, -m);
@@ -696,30 +699,45 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             pair_sync();   // the flags have been read: the maxima go to the same place
         }
         if (!done) {
-          if constexpr (CAP)
-            cap_scores(cc, x);
-          else {
-#pragma unroll
-            for (int e = 0; e < KH; ++e) x[e] *= sc;
-          }
+          if constexpr (CAP) cap_scores(cc, x);
           if constexpr (BIAS) {
             const float d0 = (float)(p - j0);
+            if (__all_sync(0xffffffffu, d0 <= 0.f || d0 >= (float)(KH - 1))) {   // linear on one side of p
+              const float sl = d0 > 0.f ? -slope2 : slope2, base = sl * d0;
+              const float2 sl2 = make_float2(-sl, -sl), b2 = make_float2(base, base);
 #pragma unroll
-            for (int e = 0; e < KH; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), x[e]);
+              for (int e = 0; e < KH; e += 2) {
+                const float2 v = make_float2(x[e], x[e + 1]);
+                const float2 d = __ffma2_rn(sl2, make_float2((float)e, (float)(e + 1)), b2);
+                const float2 y = CAP ? __fadd2_rn(v, d) : __ffma2_rn(v, cc.lin, d);
+                x[e] = y.x;
+                x[e + 1] = y.y;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < KH; ++e) x[e] = fmaf(-slope2, fabsf(d0 - (float)e), CAP ? x[e] : x[e] * sc);
+            }
+          } else if constexpr (!CAP) {
+#pragma unroll
+            for (int e = 0; e < KH; e += 2) {
+              const float2 y = __fmul2_rn(make_float2(x[e], x[e + 1]), cc.lin);
+              x[e] = y.x;
+              x[e + 1] = y.y;
+            }
           }
-          if (masked) {
+          if (cut) {
 #pragma unroll
             for (int e = 0; e < KH; ++e)
               if (j0 + e > last) x[e] = -INFINITY;
-            if (!one_doc) {
+          }
+          if (!one_doc) {
 #pragma unroll
-              for (int e = 0; e < KH; e += 4) {
-                const int4 d = *reinterpret_cast<const int4*>(dbuf + e);
-                if (d.x != qdoc || qdoc < 0) x[e] = -INFINITY;
-                if (d.y != qdoc || qdoc < 0) x[e + 1] = -INFINITY;
-                if (d.z != qdoc || qdoc < 0) x[e + 2] = -INFINITY;
-                if (d.w != qdoc || qdoc < 0) x[e + 3] = -INFINITY;
-              }
+            for (int e = 0; e < KH; e += 4) {
+              const int4 d = *reinterpret_cast<const int4*>(dbuf + e);
+              if (d.x != qdoc) x[e] = -INFINITY;
+              if (d.y != qdoc) x[e + 1] = -INFINITY;
+              if (d.z != qdoc) x[e + 2] = -INFINITY;
+              if (d.w != qdoc) x[e + 3] = -INFINITY;
             }
           }
           xm[half * TILE + lrow] = max_of(x);
