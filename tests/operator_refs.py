@@ -15,13 +15,13 @@ def rows_ref(t):
     return t * 127 / safe[:, None], top / 127
 
 
-def check_rows(q, scale, t, what, sum_terms=0, near=3e-5):
+def check_rows(q, scale, t, what, sum_terms=0, near=3.1e-5):
     """q and scale of a kernel against float64 rows t.
 
-    The kernel's 127 t / max|t| carries at most three fp32 roundings (the product with gamma,
-    its maximum, the quotient) before the one that makes it whole: 127 * 3 * 2^-24 = 2.3e-5
-    of a step, so q may differ from the rounded float64 value only where that value is
-    within 3e-5 of a tie.  scale: one rounding, and with a norm those of a sum of
+    The kernel's t (127 / max|t|) carries at most four fp32 roundings (the product with gamma,
+    its maximum, the quotient, the product) before the one that makes it whole: 127 * 4 * 2^-24
+    = 3.03e-5 of a step, so q may differ from the rounded float64 value only where that value
+    is within 3.1e-5 of a tie.  scale: one rounding, and with a norm those of a sum of
     `sum_terms` squares added in order, halved by the root, and five more."""
     u, s = rows_ref(t.cpu())
     q, scale = q.cpu().double(), scale.cpu().double()

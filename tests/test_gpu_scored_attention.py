@@ -45,7 +45,7 @@ SHAPES = [
     # B, Sq, Sk, Hq, Hkv, D
     (1, 1, 1, 1, 1, 128), (2, 1, 130, 4, 2, 64), (1, 3, 127, 7, 1, 128), (2, 31, 31, 8, 8, 128), (1, 128, 128, 2, 2, 64),
     (1, 129, 129, 1, 1, 128), (1, 151, 151, 2, 1, 128), (1, 257, 300, 3, 1, 64), (1, 65, 513, 4, 2, 128), (3, 2, 700, 8, 2, 128),
-    (1, 300, 300, 2, 2, 64),
+    (1, 300, 300, 2, 2, 64), (1, 100, 1500, 2, 2, 128), (1, 16, 257, 2, 1, 64), (2, 20, 600, 3, 3, 128), (1, 130, 1100, 2, 1, 128),
 ]
 
 
@@ -66,9 +66,10 @@ def test_all_options(shape, dtype):
 
 
 @pytest.mark.parametrize("option", [dict(cap=50.0), dict(cap=0.7), dict(causal=True),
-                                    dict(slopes=torch.tensor([0.0, 0.5, 2.0, 0.01], dtype=torch.float32)), dict(scale=0.0), dict(scale=-0.3)])
+                                    dict(slopes=torch.tensor([0.0, 0.5, 2.0, 0.01], dtype=torch.float32)), dict(scale=0.0), dict(scale=-0.3), dict(scale=-0.3, cap=4.0), dict(scale=0.0, cap=4.0),
+                                    dict(cap=30.0, slopes=torch.tensor([0.3, -0.02, 0.0, 0.004], dtype=torch.float32))])
 @pytest.mark.parametrize("dtype", [BF16, FP32])
-@pytest.mark.parametrize("Sq,Sk", [(200, 200), (5, 400)])
+@pytest.mark.parametrize("Sq,Sk", [(200, 200), (5, 400), (140, 1200)])
 def test_one_option(Sq, Sk, dtype, option):
     option = {n: v.cuda() if torch.is_tensor(v) else v for n, v in option.items()}
     _run(Sq + Sk, (2, Sq, Sk, 4, 2, 128), dtype, **option)
@@ -210,3 +211,85 @@ def test_two_captured_graphs():
     for w, o in zip(want, outs):
         assert torch.equal(w, o)
     kb.kernel_status()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_offsets_past_32_bits(dtype):
+    """A batch stride of 2^31 elements in the cache, the queries and the output."""
+    require_cuda()
+    g = torch.Generator().manual_seed(12)
+    far = 1 << 31
+    buf = torch.empty(far + 4 * 40000, dtype=dtype, device="cuda")
+
+    def view(at, tokens, heads):
+        v = buf.as_strided((2, tokens, heads, 64), (far, heads * 64, 64, 1), at)
+        v.copy_(torch.randn(2, tokens, heads, 64, generator=g).to(dtype))
+        return v
+
+    for Sq in (3, 150):
+        k, v, q, out = view(0, 200, 1), view(40000, 200, 1), view(80000, Sq, 2), view(120000, Sq, 2)
+        check_attention(kb.attention_scored(q, k, v, causal=True, out=out), q, k, v, causal=True)
+    del buf, k, v, q, out
+
+
+def test_more_key_tiles_than_the_document_list_holds():
+    """Over 4096 key tiles of documents: every tile is gone through with its mask."""
+    Sk = 4096 * 128 + 300
+    q, k, v = _qkv(15, 1, 70, Sk, 1, 1, 64, BF16)
+    kd = (torch.arange(Sk, dtype=torch.int32) // 200000)[None].cuda().contiguous()
+    qd = (torch.arange(70, dtype=torch.int32) % 4 - 1)[None].cuda().contiguous()
+    out = kb.attention_scored(q, k, v, q_documents=qd, kv_documents=kd)
+    at = [0, 1, 2, 3, 33, 69]
+    check_attention(out[:, at], q[:, at], k, v, q_documents=qd[:, at], kv_documents=kd)
+
+
+def test_documents_split_over_ctas():
+    """Few CTAs, so that the keys are split: lists of parts, empty parts, and their join."""
+    d = (torch.arange(3000, dtype=torch.int32) // 170)[None].cuda().contiguous()
+    qd = d[:, 1400:1570].contiguous()
+    q, k, v = _qkv(16, 1, 170, 3000, 1, 1, 128, BF16)
+    check_attention(kb.attention_scored(q, k, v, q_documents=qd, kv_documents=d, slopes=torch.tensor([0.05]).cuda()), q, k, v,
+                    q_documents=qd, kv_documents=d, slopes=torch.tensor([0.05]))
+
+
+def test_a_workspace_that_is_missing_or_short_is_refused():
+    import ctypes
+    q, k, v = _qkv(17, 1, 1, 3000, 8, 2, 128, BF16)
+    out = torch.empty_like(q)
+    lib = kb.load_library()
+    s = [tuple(t.stride()[:3]) for t in (q, k, v, out)]
+    a = kb.ScoredAttention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None, None, None, None, None, None, *s,
+                           1, 1, 3000, 8, 2, 128, kb.BF16, 0, 0.1, 0.0)
+    n = ctypes.c_size_t()
+    assert lib.kimodo_attention_scored_workspace(ctypes.byref(a), ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.kimodo_attention_scored(ctypes.byref(a), None, 0, None) == -1
+    assert b"workspace" in lib.kimodo_last_error()
+    ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+    assert lib.kimodo_attention_scored(ctypes.byref(a), ws.data_ptr(), n.value - 1, None) == -1
+    host = torch.empty(16, dtype=torch.int32)
+    a.kv_lengths = host.data_ptr()
+    assert lib.kimodo_attention_scored(ctypes.byref(a), ws.data_ptr(), n.value, None) == -1   # host memory
+
+
+def test_binding_checks():
+    q, k, v = _qkv(18, 2, 4, 9, 4, 2, 64, BF16)
+    for bad, text in ((dict(q=q.half()), "bf16 or fp32"), (dict(k=k.float()), "agree"), (dict(v=v[:, :8]), "agree"),
+                      (dict(q=q[0]), "4-D"), (dict(q=q.transpose(2, 3)), "agree"), (dict(k=k.cpu(), v=v), "must be on cuda")):
+        t = dict(q=q, k=k, v=v) | bad
+        with pytest.raises(ValueError, match=text):
+            kb.attention_scored(t["q"], t["k"], t["v"])
+    for bad, text in ((dict(slopes=torch.ones(3).cuda()), "slopes"), (dict(prefix=_i32(1), causal=True), "prefix"),
+                      (dict(kv_lengths=torch.ones(2, dtype=torch.int64).cuda()), "kv_lengths"), (dict(q_start=torch.zeros(2, dtype=torch.int32)), "q_start"),
+                      (dict(out=torch.empty(1).cuda()), "out")):
+        with pytest.raises(ValueError, match=text):
+            kb.attention_scored(q, k, v, **bad)
+    for bad, text in ((dict(prefix=_i32(1, 1)), "prefix needs causal"), (dict(q_documents=torch.zeros(2, 4, dtype=torch.int32).cuda()), "together"),
+                      (dict(cap=-2.0), "cap"), (dict(scale=float("inf")), "scale"), (dict(scale=1e7, cap=1.0), "millionth")):
+        with pytest.raises(kb.KimodoError, match=text):
+            kb.attention_scored(q, k, v, **bad)
+    with pytest.raises(kb.KimodoError, match="strides"):
+        kb.attention_scored(q, k[:1].expand(2, -1, -1, -1), v)
+    with pytest.raises(kb.KimodoError, match="16-byte aligned"):
+        kb.attention_scored(q.flatten()[4:4 + 256].view(1, 1, 4, 64), k[:1], v[:1])
+    with pytest.raises(kb.KimodoError, match="head_dim"):
+        kb.attention_scored(q[..., :32].contiguous(), k[..., :32].contiguous(), v[..., :32].contiguous())

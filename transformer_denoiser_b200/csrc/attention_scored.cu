@@ -423,9 +423,9 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   auto entry = [&](int n) -> int { return listed ? list[n] : n << 4 | (docs ? 5 : 15); };
   auto takes = [&](int t, int e) -> bool { return jt0 + (e >> 4) < (t ? end1 : end0) && ((e >> (2 * t)) & 1); };
 
-  // registers: 640 x 96 at launch cover 128 x 64 + 512 x 104
+  // registers: 640 x 96 at launch cover 128 x 32 + 512 x 112
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0) {
       if (lane == 0) {
         // ---------------- TMA: K and V tile of every key tile that a row tile takes
@@ -585,7 +585,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     // ---------------- softmax and output of row tile t_own
     const int t = t_own;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;

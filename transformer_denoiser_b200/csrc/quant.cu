@@ -189,9 +189,9 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, NORM && TPR == 256 ? 5 
     }
   }
   if (t == 0) a.scale[row] = !finite ? __uint_as_float(0x7fc00000u) : top == 0 ? 0.f : scale;
-  // q = rint(127 t / max |t|): adding 1.5 * 2^23 leaves the rounded integer (ties to even) in
-  // the low bits of the sum, with one rounding for product and sum together.  A maximum near
-  // the smallest floats is scaled up first, so that 127 / max stays finite.
+  // q = rint(t * (127 / max |t|)), quotient and product in fp32: adding 1.5 * 2^23 leaves the
+  // rounded integer (ties to even) in the low bits of the sum.  A maximum near the smallest
+  // floats is scaled up first, so that 127 / max stays finite.
   const float up = amax < 0x1p-100f ? 0x1p100f : 1.f;
   const float inv = finite && top != 0 ? 127.f / (amax * up) : 0.f;
   int8_t* q = a.q + row * a.ldq;
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, NORM && TPR == 256 ? 5 
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float v = (NORM ? h[i][e] * g[NORM ? i : 0][e] : h[i][e]) * up;
-      b[e] = finite ? __float_as_uint(fmaf(v, inv, 12582912.f)) : 0u;
+      b[e] = finite ? __float_as_uint(__fadd_rn(__fmul_rn(v, inv), 12582912.f)) : 0u;
     }
     if constexpr (VEC) {
       const int c = column(i, 0);
