@@ -1243,28 +1243,24 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
 // ---------------------------------------------------------------- fp32
 //
-// The fp32 path on the FMA units (the tensor cores have no fp32 kind, and tf32 rounds too
-// much).  A CTA takes BM rows and walks key tiles of FT: thread (row group, column group) holds
-// TM x 4 scores and TM x 4 HD / FT outputs in registers.  A 16-byte shared-memory load costs
-// four cycles of the SM's one port whatever its lanes share, in which the FMA units do 16
-// multiplications a lane, so shared memory bounds these tiles (4 rows: 8 loads for 64
-// multiplications of the scores, 12 for 128 of the outputs).  Rows are padded by 16 bytes,
-// so that the eight lanes of a load's phase read different banks; the weights take the keys'
-// place.  A row's statistics live in the lanes that share it.
-// Many rows: 64 rows (256 threads, 4 rows each) by 64 keys; where blocks of 64 would leave over a
-// tenth of the rows idle, 32 rows by 32 keys (32 x 8 heads x 151 tokens, ragged: 137 us
-// against 160; 16 heads x 1000 tokens: 355 against 262); at most 16 rows: 16 by 64.
-template <int HD, int TM, int NT, int FT>
+// At most 16 rows (new tokens over a cache) on the FMA units, where the keys' and values' bytes
+// count: a CTA of 128 threads takes 16 rows and walks key tiles of 64; thread (row group,
+// column group) holds 2 x 4 scores and 2 x HD / 16 outputs in registers.  Rows are padded by
+// 16 bytes, so that the eight lanes of a load's phase read different banks; the weights take
+// the keys' place.  A row's statistics live in the 16 lanes that share it.  (2 x 32 heads over
+// 8000 keys, 8 key heads: 58 us for 131 MB.)
+constexpr int FT = 64, TM = 2, NT = 128;
+template <int HD>
 struct F32Cfg {
   static constexpr int CG = FT / 4, RG = NT / CG, BM = RG * TM, LD = HD + 4, LP = FT + 4;
   static_assert(BM * (FT + 4) <= FT * (HD + 4), "the weights fit in the keys' place");
   static constexpr size_t SMEM = (size_t)(BM * LD + 2 * FT * LD) * 4;
 };
 
-template <int HD, int TM, int NT, int FT>
-__global__ void __launch_bounds__(NT, FT == 32 ? 4 : 2) scored_f32_kernel(const __grid_constant__ ScoredAttention a,
+template <int HD>
+__global__ void __launch_bounds__(NT, 2) scored_f32_kernel(const __grid_constant__ ScoredAttention a,
                                                             const __grid_constant__ ScoredPlan plan) {
-  using C = F32Cfg<HD, TM, NT, FT>;
+  using C = F32Cfg<HD>;
   constexpr int CG = C::CG, RG = C::RG, BM = C::BM, LD = C::LD, LP = C::LP, ND = HD / (4 * CG);   // float4 of outputs per row and thread
   extern __shared__ float fsm[];
   float* sQ = fsm;
@@ -1464,6 +1460,385 @@ __global__ void __launch_bounds__(NT, FT == 32 ? 4 : 2) scored_f32_kernel(const 
   }
 }
 
+// ---------------------------------------------------------------- fp32 on the tensor cores
+//
+// For more than 16 rows the fp32 path runs on the bf16 tensor cores with every operand in
+// three bf16 parts, x = x0 + x1 + x2, each the rounding of what the parts before leave: 24
+// bits, as fp32 has.  Of the nine products of two such sums the six down to 2^-16 are formed
+// (those left out are below 2^-24 of the largest) and added in fp32, smallest first.  Six
+// MMAs at over 16 times the FMA units' rate: 16 heads x 1000 tokens 65 us against 262 in register
+// tiles on the FMA units, 32 x 8 heads x 151 tokens 81 against 137 (two CTAs a head, the
+// second with 23 rows: set-up and latencies).
+// One 128-row tile a CTA, key tiles of 64.  Roles (544 threads): warps 0-7 softmax and output
+// (two threads a row, 32 keys each), warps 8-11 and 12-15 load keys and values, split them and
+// write them as the MMAs read them (128-byte swizzle), warp 16 MMA.  TMEM: two score buffers
+// of 64 columns, the three weight parts in 32 each, the output.
+constexpr int S3_THREADS = 544;
+constexpr int S3_KEYS = 64;
+template <int HD>
+struct Split3Cfg {
+  static constexpr uint32_t Q_PART = TILE * HD * 2, KV_PART = S3_KEYS * HD * 2;
+  static constexpr uint32_t Q_HALF = TILE * 128, KV_HALF = S3_KEYS * 128;   // 64 dims
+  static constexpr size_t BODY = 3 * Q_PART + 6 * KV_PART;
+  // exchange of maxima and sums (2 turns x 2 halves x 128 rows), documents (8 warps x 32 keys)
+  static constexpr size_t XCH = 4 * TILE * 4 + 8 * 32 * 4;
+  static constexpr size_t SMEM = 1024 + BODY + XCH + 16 * 8 + 16;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+// (part of the first operand, part of the second), smallest products first
+__device__ constexpr int S3_A[6] = {2, 0, 1, 1, 0, 0}, S3_B[6] = {0, 2, 1, 0, 1, 0};
+
+// Eight floats in three bf16 parts.
+__device__ __forceinline__ void split3(const float (&v)[8], uint4 (&out)[3]) {
+  float r[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = v[e];
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[e] = bf16x2_bits(r[2 * e], r[2 * e + 1]);
+      r[2 * e] -= __uint_as_float(w[e] << 16);
+      r[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+    }
+    out[t] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(S3_THREADS, 1)
+scored_split3_kernel(const __grid_constant__ ScoredAttention a, const __grid_constant__ ScoredPlan plan, DevError* err) {
+  using C = Split3Cfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sQ = ptx::smem_u32(smem), sK = sQ + 3 * C::Q_PART, sV = sK + 3 * C::KV_PART;
+  float* xch = reinterpret_cast<float*>(smem + C::BODY);
+  int* docs_smem = reinterpret_cast<int*>(xch + 4 * TILE);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(docs_smem + 8 * 32);
+  const uint32_t bar0 = ptx::smem_u32(bars);
+  // full (loaders' warps), empty (MMA) of keys and values; scores; weights; output; drain
+  const uint32_t k_full = bar0, k_empty = bar0 + 8, v_full = bar0 + 16, v_empty = bar0 + 24, p_bar = bar0 + 48,
+                 o_bar = bar0 + 56, drain_bar = bar0 + 64, q_bar = bar0 + 72;
+  auto s_bar = [&](int i) { return bar0 + 32u + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  constexpr uint32_t tmem_base = 0, P_COL = 128, O_COL = 256;   // all columns are this CTA's
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long id = blockIdx.x;
+  const int split = (int)(id % plan.splits);
+  id /= plan.splits;
+  const int hk = (int)(id % a.Hkv);
+  id /= a.Hkv;
+  const int b = (int)(id % a.B);
+  const int rb = plan.row_blocks - 1 - (int)(id / a.B);
+  const int rows = a.Sq * a.G, row0 = rb * TILE;
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(k_full, 4);
+    ptx::mbar_init(k_empty, 1);
+    ptx::mbar_init(v_full, 4);
+    ptx::mbar_init(v_empty, 1);
+    ptx::mbar_init(s_bar(0), 1);
+    ptx::mbar_init(s_bar(1), 1);
+    ptx::mbar_init(p_bar, 8);
+    ptx::mbar_init(o_bar, 1);
+    ptx::mbar_init(drain_bar, 1);
+    ptx::mbar_init(q_bar, 8);
+    ptx::fence_mbar_init();
+    *abort = 0;
+  }
+  if (warp == 16) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::pdl_wait();
+  ptx::pdl_trigger();
+  const SeqInfo seq = sequence_info(a, b);
+  constexpr int CH = HD / 8;                                // 8-dim chunks of a row
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const int row_last = min(row0 + TILE, rows) - 1;
+  const int key_end = 1 + last_key(a, seq, (long)seq.start + row_last / a.G);
+  const int jt_all = (key_end + S3_KEYS - 1) / S3_KEYS;
+  const int jt0 = min(split * plan.tiles_per_split, jt_all), jt1 = min(jt0 + plan.tiles_per_split, jt_all);
+  const int n_tiles = jt1 - jt0;
+
+  if (warp >= 8 && warp < 16) {
+    // ---------------- loads: one operand's tile, split into its parts
+    const bool values = warp >= 12;
+    const int l = threadIdx.x - (values ? 384 : 256);
+    const long stride = values ? a.v_token : a.k_token;
+    const float* src = values ? static_cast<const float*>(a.v) + b * a.v_batch + hk * a.v_head
+                              : static_cast<const float*>(a.k) + b * a.k_batch + hk * a.k_head;
+    uint8_t* dst = smem + 3 * C::Q_PART + (values ? 3 * C::KV_PART : 0);
+    const uint32_t full = values ? v_full : k_full, empty = values ? v_empty : k_empty;
+    constexpr int TASKS = S3_KEYS * CH / 128;
+    bool ok = true;
+    for (int n = 0; n < n_tiles && ok; ++n) {
+      const int j0 = (jt0 + n) * S3_KEYS;
+      float4 lo[TASKS], hi[TASKS];
+#pragma unroll
+      for (int u = 0; u < TASKS; ++u) {
+        const int task = l + 128 * u, j = j0 + task / CH;
+        lo[u] = hi[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < seq.kv_len) {
+          const float* p = src + j * stride + (task % CH) * 8;
+          lo[u] = *reinterpret_cast<const float4*>(p);
+          hi[u] = *reinterpret_cast<const float4*>(p + 4);
+        }
+      }
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(empty, (n & 1) ^ 1u, abort, WAIT_LIMIT_NS));
+      if (!ok) break;
+#pragma unroll
+      for (int u = 0; u < TASKS; ++u) {
+        const int task = l + 128 * u, r = task / CH, ch = task % CH;
+        const float v[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+        uint4 w[3];
+        split3(v, w);
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          *reinterpret_cast<uint4*>(dst + t * C::KV_PART + (ch >> 3) * C::KV_HALF + r * 128 +
+                                    (((ch & 7) ^ (r & 7)) << 4)) = w[t];
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full);
+    }
+    if (!ok && !*abort && lane == 0) record_timeout(err, abort);
+  } else if (warp == 16) {
+    // ---------------- MMA: S of a tile ahead of P V of the one before
+    const uint32_t idesc_s = ptx::idesc_bf16_f32(TILE, S3_KEYS);
+    const uint32_t idesc_o = ptx::idesc_bf16_f32(TILE, HD) | (1u << 16);
+    const uint64_t d_q = ptx::smem_desc_sw128(sQ), d_k = ptx::smem_desc_sw128(sK), d_v = desc_mn(sV, C::KV_HALF);
+    const uint32_t k_hi = (uint32_t)(d_k >> 32), v_hi = (uint32_t)(d_v >> 32);
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t ph) {
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, ph, abort, WAIT_LIMIT_NS));
+      return ok;
+    };
+    auto qk = [&](int n) {
+      if (!wait(k_full, n & 1)) return;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int t = 0; t < 6; ++t) {
+          const uint32_t q = (uint32_t)d_q + S3_A[t] * (C::Q_PART >> 4), k = (uint32_t)d_k + S3_B[t] * (C::KV_PART >> 4);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            ptx::tc_mma_bf16_lo(tmem_base + (n & 1) * S3_KEYS, q + (((kk >> 2) * C::Q_HALF + (kk & 3) * 32) >> 4),
+                                k + (((kk >> 2) * C::KV_HALF + (kk & 3) * 32) >> 4), k_hi, idesc_s, (t | kk) != 0);
+        }
+        ptx::tc_commit(s_bar(n & 1));
+        ptx::tc_commit(k_empty);
+      }
+      __syncwarp();
+    };
+    if (n_tiles > 0 && wait(q_bar, 0)) qk(0);
+    for (int n = 0; n < n_tiles && ok; ++n) {
+      if (n + 1 < n_tiles) qk(n + 1);
+      if (!ok || !wait(v_full, n & 1) || !wait(p_bar, n & 1)) break;
+      ptx::tc_fence_after();
+      const uint32_t more = n != 0 ? 1u : 0u;
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int t = 0; t < 6; ++t) {
+          const uint32_t v = (uint32_t)d_v + S3_B[t] * (C::KV_PART >> 4);
+#pragma unroll
+          for (int kk = 0; kk < S3_KEYS / 16; ++kk)
+            ptx::tc_mma_bf16_ta_lo(tmem_base + O_COL, tmem_base + P_COL + S3_A[t] * 32 + kk * 8, v + kk * (2048 >> 4), v_hi,
+                                   idesc_o, (t | kk) != 0 ? 1u : more);
+        }
+        ptx::tc_commit(v_empty);
+        ptx::tc_commit(o_bar);
+      }
+      __syncwarp();
+    }
+    if (!ok && !*abort && lane == 0) record_timeout(err, abort);
+    if (ptx::elect_one()) {
+      ptx::tc_commit(drain_bar);
+      volatile int never = 0;
+      if (!ptx::mbar_wait_bounded(drain_bar, 0, &never, WAIT_LIMIT_NS)) record_timeout(err, abort);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- queries in their parts, while the first keys and values are on their way
+    {
+      const float* qb = static_cast<const float*>(a.q) + b * a.q_batch + (long)hk * a.G * a.q_head;
+#pragma unroll 4
+      for (int c = threadIdx.x; c < TILE * CH; c += 256) {
+        const int lr = c / CH, ch = c % CH, r = row0 + lr;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (r < rows) {
+          const int i = r / a.G, g = r - i * a.G;
+          const float* q = qb + i * a.q_token + g * a.q_head + ch * 8;
+          const float4 x = *reinterpret_cast<const float4*>(q), y = *reinterpret_cast<const float4*>(q + 4);
+          v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        }
+        uint4 w[3];
+        split3(v, w);
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          *reinterpret_cast<uint4*>(smem + t * C::Q_PART + (ch >> 3) * C::Q_HALF + lr * 128 +
+                                    (((ch & 7) ^ (lr & 7)) << 4)) = w[t];
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(q_bar);
+    }
+    // ---------------- softmax and output: row lrow, keys 32 half .. of a tile, dims HD / 2 half ..
+    const int quarter = warp & 3, half = warp >> 2, lrow = quarter * 32 + lane;
+    constexpr int KH = S3_KEYS / 2, DH2 = HD / 2;
+    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t o_addr = tmem_base + lane_addr + O_COL;
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
+    const int r_own = row0 + lrow;
+    const bool row_ok = r_own < rows;
+    const int i_own = row_ok ? r_own / a.G : 0, g_own = row_ok ? r_own - i_own * a.G : 0;
+    const int p = seq.start + i_own;
+    const int last = row_ok ? last_key(a, seq, (long)seq.start + i_own) : -1;
+    const bool docs = a.q_doc != nullptr;
+    int qdoc = docs && row_ok ? a.q_doc[(long)b * a.Sq + i_own] : 0;
+    qdoc = qdoc < 0 ? -2 : qdoc;   // a key in no document is staged as -1
+    const float slope2 = a.slopes && row_ok ? a.slopes[hk * a.G + g_own] * LOG2E : 0.f;
+    int* dbuf = docs_smem + warp * 32;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int n = 0; n < n_tiles; ++n) {
+      const int j0 = (jt0 + n) * S3_KEYS + half * KH;
+      if (docs) {
+        __syncwarp();   // the documents before have been read
+        dbuf[lane] = max(a.kv_doc[(long)b * a.Sk + min(j0 + lane, a.Sk - 1)], -1);
+        __syncwarp();
+      }
+      // (after a wait that ran out the rest is gone through without waiting, so that the
+      // barriers of the warp pairs stay matched)
+      if (ok) ok = ptx::mbar_wait_bounded(s_bar(n & 1), (n >> 1) & 1, abort, WAIT_LIMIT_NS);
+      ptx::tc_fence_after();
+      float x[KH];
+      ptx::tmem_ld32(tmem_base + lane_addr + (n & 1) * S3_KEYS + half * KH, x);
+      ptx::tmem_ld_wait();
+      if (a.cap > 0.f) {
+#pragma unroll
+        for (int e = 0; e < KH; ++e) x[e] = a.cap * tanhf(x[e] * a.scale / a.cap) * LOG2E;
+      } else {
+#pragma unroll
+        for (int e = 0; e < KH; ++e) x[e] = x[e] * a.scale * LOG2E;
+      }
+      if (a.slopes) {
+#pragma unroll
+        for (int e = 0; e < KH; ++e) x[e] = fmaf(-slope2, fabsf((float)(p - j0 - e)), x[e]);
+      }
+      if (!__all_sync(0xffffffffu, j0 + KH - 1 <= last)) {
+#pragma unroll
+        for (int e = 0; e < KH; ++e)
+          if (j0 + e > last) x[e] = -INFINITY;
+      }
+      if (docs) {
+#pragma unroll
+        for (int e = 0; e < KH; ++e)
+          if (dbuf[e] != qdoc) x[e] = -INFINITY;
+      }
+      float* xm = xch + (n & 1) * 2 * TILE;
+      xm[half * TILE + lrow] = max_of(x);
+      pair_sync();
+      const float top = max3(xm[lrow], xm[TILE + lrow], m);
+      const bool move = n == 0 || !(top <= m + RESCALE_AT);
+      const float m_new = move ? top : m;
+      if (n > 0) {
+        if (ok) ok = ptx::mbar_wait_bounded(o_bar, (n - 1) & 1, abort, WAIT_LIMIT_NS);   // weights and output of tile n - 1
+        if (__any_sync(0xffffffffu, move)) {
+          ptx::tc_fence_after();
+          const float f = m_new == m ? 1.f : exp2f(m - m_new);   // m = -infinity: 0
+          l *= f;
+#pragma unroll 1
+          for (int c = half * DH2; c < (half + 1) * DH2; c += 16) {
+            float v[16];
+            uint32_t w[16];
+            ptx::tmem_ld(o_addr + c, v);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * f);
+            ptx::tmem_st16(o_addr + c, w);
+          }
+        }
+      }
+      m = m_new;
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int e = 0; e < KH; ++e) {
+        x[e] = exp2f(x[e] - ref);
+        l += x[e];
+      }
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          w[e] = bf16x2_bits(x[2 * e], x[2 * e + 1]);
+          x[2 * e] -= __uint_as_float(w[e] << 16);
+          x[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+        }
+        ptx::tmem_st16(tmem_base + lane_addr + P_COL + t * 32 + half * 16, w);
+      }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(p_bar);
+    }
+    if (ok && n_tiles > 0) ok = ptx::mbar_wait_bounded(o_bar, (n_tiles - 1) & 1, abort, WAIT_LIMIT_NS);
+    if (!ok && !*abort) record_timeout(err, abort);
+    pair_sync();   // the maxima have been read
+    xch[half * TILE + lrow] = l;
+    pair_sync();
+    l = xch[lrow] + xch[TILE + lrow];
+    ptx::tc_fence_after();
+    const bool seen = n_tiles > 0 && l != 0.f;   // l is NaN where a score is
+    bool finite = true;
+    const long n_rows = (long)a.B * a.Hkv * rows, prow = ((long)b * a.Hkv + hk) * rows + r_own;
+    float* o = plan.parts == 1 ? static_cast<float*>(a.out) + b * a.o_batch + i_own * a.o_token + (long)(hk * a.G + g_own) * a.o_head
+                               : plan.part_o + ((long)split * n_rows + prow) * HD;
+    const bool write = ok && row_ok && (plan.parts == 1 || seen);
+    const float inv = 1.f / l;
+#pragma unroll 1
+    for (int c = half * DH2; c < (half + 1) * DH2; c += 16) {
+      float v[16];
+      ptx::tmem_ld(o_addr + c, v);
+      ptx::tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        v[e] = seen ? v[e] * inv : 0.f;
+        finite = finite && fabsf(v[e]) < INFINITY;
+      }
+      if (write) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<float4*>(o + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      }
+    }
+    if (plan.parts == 1) {
+      pair_sync();   // the sums have been read; both halves are written
+      xch[half * TILE + lrow] = finite ? 0.f : 1.f;
+      pair_sync();
+      unsigned redo = half == 0 && ok ? __ballot_sync(0xffffffffu, row_ok && xch[lrow] + xch[TILE + lrow] != 0.f) : 0u;
+      while (redo) {
+        const int src = __ffs(redo) - 1;
+        redo &= redo - 1;
+        row_by_warp<float, HD>(a, b, hk * a.G + __shfl_sync(0xffffffffu, g_own, src), __shfl_sync(0xffffffffu, i_own, src));
+      }
+    } else if (row_ok && half == 0) {
+      plan.part_lse[(long)split * n_rows + prow] = seen ? m + log2f(l) : -INFINITY;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(*tmem_slot, TMEM_COLS);
+  }
+}
+
 // ---------------------------------------------------------------- join of the parts
 // o = sum 2^(lse - max) o_part / sum 2^(lse - max).  One CTA a row: warp w takes parts w, w + 4, ...
 template <typename T, int HD>
@@ -1568,10 +1943,22 @@ cudaError_t run_tc(const ScoredAttention& a, const ScoredPlan& plan, DevError* e
   return e != cudaSuccess ? e : join<bf16, HD>(a, plan, st);
 }
 
-template <int HD, int TM, int NT, int FT>
+template <int HD>
+cudaError_t launch_split3(const ScoredAttention& a, const ScoredPlan& plan, DevError* err, cudaStream_t st) {
+  using C = Split3Cfg<HD>;
+  auto kern = scored_split3_kernel<HD>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long grid = (long)plan.row_blocks * a.Hkv * a.B * plan.splits;
+  if (grid > INT_MAX) return cudaErrorInvalidValue;
+  e = launch_kernel(kern, dim3((unsigned)grid), dim3(S3_THREADS), C::SMEM, st, a, plan, err);
+  return e != cudaSuccess ? e : join<float, HD>(a, plan, st);
+}
+
+template <int HD>
 cudaError_t launch_f32(const ScoredAttention& a, const ScoredPlan& plan, cudaStream_t st) {
-  using C = F32Cfg<HD, TM, NT, FT>;
-  auto kern = scored_f32_kernel<HD, TM, NT, FT>;
+  using C = F32Cfg<HD>;
+  auto kern = scored_f32_kernel<HD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return e;
   const long grid = (long)plan.row_blocks * a.Hkv * a.B * plan.splits;
@@ -1596,11 +1983,10 @@ ScoredPlan scored_attention_plan(const ScoredAttention& a, bool is_bf16, int num
     fill = p.few ? 4 : 1;
     least = 2;
   } else {
-    const long r64 = (rows + 63) / 64 * 64, r32 = (rows + 31) / 32 * 32;
-    p.few = rows <= 16 ? 16 : r64 * 10 > r32 * 11 ? 32 : 64;
-    block = p.few;
-    tile = p.few == 32 ? 32 : 64;
-    fill = 2;
+    p.few = rows <= 16 ? 16 : 0;
+    block = p.few ? 16 : TILE;
+    tile = 64;
+    fill = p.few ? 2 : 1;
     least = 2;
   }
   p.k = scored_const(a.scale, a.cap);
@@ -1625,9 +2011,8 @@ cudaError_t attention_scored(const ScoredAttention& a, bool is_bf16, ScoredPlan 
     plan.part_lse = plan.part_o + (size_t)plan.parts * a.B * a.Hq * a.Sq * a.HD;
   }
   if (is_bf16) return a.HD == 64 ? run_tc<64>(a, plan, err, st) : run_tc<128>(a, plan, err, st);
-  if (plan.few == 16) return a.HD == 64 ? launch_f32<64, 2, 128, 64>(a, plan, st) : launch_f32<128, 2, 128, 64>(a, plan, st);
-  if (plan.few == 32) return a.HD == 64 ? launch_f32<64, 2, 128, 32>(a, plan, st) : launch_f32<128, 2, 128, 32>(a, plan, st);
-  return a.HD == 64 ? launch_f32<64, 4, 256, 64>(a, plan, st) : launch_f32<128, 4, 256, 64>(a, plan, st);
+  if (!plan.few) return a.HD == 64 ? launch_split3<64>(a, plan, err, st) : launch_split3<128>(a, plan, err, st);
+  return a.HD == 64 ? launch_f32<64>(a, plan, st) : launch_f32<128>(a, plan, st);
 }
 
 }  // namespace kd

@@ -183,7 +183,7 @@ struct ScoredConst {
 // workspace of `bytes`, joined by a second kernel.
 struct ScoredPlan {
   int splits = 1, tiles_per_split = 1, row_blocks = 1, parts = 1;
-  int few = 0;   // bf16: rows of the kernel for few rows (0: not that one); fp32: rows of a block
+  int few = 0;   // rows of the kernel for few rows (0: not those)
   ScoredConst k;
   float* part_o = nullptr;
   float* part_lse = nullptr;
