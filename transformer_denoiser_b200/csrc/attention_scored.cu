@@ -11,11 +11,12 @@
 // Sq * G rows (token-major), so grouped heads share every key tile they load and a few new
 // tokens fill one MMA tile together.
 //
-// Many rows (scored_tc_kernel): a CTA takes 256 rows as two 128-row tiles; while the softmax
-// of one runs, the tensor cores work on the other.  Roles (640 threads): warp 0 TMA of K and
+// Many rows (scored_tc_kernel): an SM works on two tiles of 128 rows, as two CTAs or as one that
+// takes both in turn; while the softmax of one runs, the tensor cores work on the other.
+// Roles (128 threads and 256 a row tile): warp 0 TMA of K and
 // V tiles (128 keys, 128-byte swizzle), warps 1 and 2 MMA issue of tile 0 and 1, warps 4-11 and 12-19 softmax and
 // output of tile 0 and 1, two threads a row, each half of the keys (one thread a row left the
-// four schedulers two warps each, too few to hide the latencies: 490 against 285 us for 16
+// four schedulers two warps each, too few to hide the latencies: 490 against 431 us for 16
 // heads x 8192 tokens).  Per key tile and row tile: S = Q K^T into 128 TMEM columns; the row's
 // threads read S, form p and write it in bf16 over S; O += P V with P as the TMEM operand.
 //
@@ -36,6 +37,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -48,8 +50,6 @@ namespace kd {
 namespace {
 
 constexpr int TILE = 128;                    // query rows of a tile, keys of a tile
-constexpr int NUM_THREADS = 640;
-constexpr int STAGES = 4;                    // K and V tiles in flight, alternating
 constexpr int MAX_LIST = 4096;               // key tiles that a CTA with documents lists (12 bits of an entry)
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr int KIMODO_ETIMEOUT_CODE = -5;
@@ -211,18 +211,25 @@ __device__ __noinline__ void row_by_warp(const ScoredAttention& a, int b, int hq
 
 // ---------------------------------------------------------------- bf16: tcgen05
 
-template <int HD>
+template <int HD, int TILES>
 struct Cfg {
+  static constexpr int THREADS = 128 + 256 * TILES;
+  // K and V tiles in flight, alternating; two CTAs share an SM where each has one row tile
+  static constexpr int STAGES = TILES == 2 || HD == 64 ? 4 : 2;
   static constexpr uint32_t Q_BYTES = TILE * HD * 2;       // one row tile
   static constexpr uint32_t KV_BYTES = TILE * HD * 2;      // one key or value tile
   static constexpr uint32_t HALF = TILE * 128;             // 64 dims of a tile
-  // HD 64 would let two CTAs share an SM, whose TMEM holds one: the size keeps them apart
-  static constexpr size_t BODY = 2 * Q_BYTES + (size_t)STAGES * KV_BYTES;
-  static constexpr size_t SMEM = 1024 + (BODY < 119808 ? 119808 : BODY) + MAX_LIST * 2 + 256 + 16 * 64 * 4 + 2 * 2 * 2 * TILE * 4;
+  static constexpr uint32_t COLS = 256 * TILES;            // TMEM
+  static constexpr size_t DATA = TILES * Q_BYTES + (size_t)STAGES * KV_BYTES;
+  // two row tiles take all of the TMEM: the size keeps a second CTA of 64-dim heads off the SM
+  static constexpr size_t BODY = TILES == 2 && DATA < 119808 ? 119808 : DATA;
+  static constexpr size_t LIST = BODY, BARS = LIST + MAX_LIST * 2, DOCS = BARS + 256, XCH = DOCS + 8 * TILES * 64 * 4;
+  static constexpr size_t SMEM = 1024 + XCH + 2 * TILES * 2 * TILE * 4;
+  static_assert(SMEM <= 232448 / (TILES == 1 ? 2 : 1) - (TILES == 1 ? 1024 : 0), "shared memory");
 };
 constexpr uint32_t TMEM_COLS = 512;
 __device__ __forceinline__ uint32_t s_col(int t) { return 128u * t; }
-template <int HD> __device__ __forceinline__ uint32_t o_col(int t) { return 256u + (uint32_t)HD * t; }
+template <int HD, int TILES> __device__ __forceinline__ uint32_t o_col(int t) { return 128u * TILES + (uint32_t)HD * t; }
 
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzle layout:
 // 64-element atoms along MN `lbo` bytes apart, 8-row groups along K 1024 bytes apart.
@@ -242,18 +249,19 @@ struct RowTile {
   int pad;
 };
 
-template <int HD, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(NUM_THREADS, 1)   // 96 registers a thread
+template <int HD, bool CAP, bool BIAS, int TILES>
+__global__ void __launch_bounds__(128 + 256 * TILES, TILES == 2 ? 1 : 2)   // 96 or 80 registers a thread
 scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ ScoredAttention a, const __grid_constant__ ScoredPlan plan,
                  DevError* err) {
-  using C = Cfg<HD>;
+  using C = Cfg<HD, TILES>;
+  constexpr int STAGES = C::STAGES, NUM_THREADS = C::THREADS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = ptx::smem_u32(smem);
-  const uint32_t sKV = sQ + 2 * C::Q_BYTES;
-  uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::BODY);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(list + MAX_LIST);
+  const uint32_t sKV = sQ + TILES * C::Q_BYTES;
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::LIST);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);
   const uint32_t bar0 = ptx::smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
@@ -265,8 +273,8 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   int* mma_lock = reinterpret_cast<int*>(tmem_slot + 2);
   int* list_len = mma_lock + 1;
   RowTile* tiles = reinterpret_cast<RowTile*>(tmem_slot + 4);
-  int* docs_smem = reinterpret_cast<int*>(smem + C::BODY + MAX_LIST * 2 + 256);   // [16 warps][64]
-  float* xch = reinterpret_cast<float*>(docs_smem + 16 * 64);                  // [2 turns][2 tiles][2 halves][TILE]
+  int* docs_smem = reinterpret_cast<int*>(smem + C::DOCS);    // [softmax warps][64]
+  float* xch = reinterpret_cast<float*>(smem + C::XCH);   // [2 turns][TILES][2 halves][TILE]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // block = ((row block, last first) * Hkv * B + (b * Hkv + hk)) * splits + split
@@ -278,12 +286,12 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const int b = (int)(id % a.B);
   const int rb = plan.row_blocks - 1 - (int)(id / a.B);
   const int rows = a.Sq * a.G;
-  const int row0 = rb * TILE * 2;
+  const int row0 = rb * TILE * TILES;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       ptx::mbar_init(full_bar(s), 1);
-      ptx::mbar_init(empty_bar(s), 2);
+      ptx::mbar_init(empty_bar(s), TILES);
     }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(s_bar(t), 1);
@@ -300,7 +308,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     ptx::tma_prefetch_desc(&tmV);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TMEM_COLS);
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::COLS);
     ptx::tmem_relinquish();
   }
   ptx::pdl_wait();
@@ -312,7 +320,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   {
     constexpr int CH = HD / 8;                               // 16-byte chunks of a row
     const bf16* qb = static_cast<const bf16*>(a.q) + b * a.q_batch + (long)hk * a.G * a.q_head;
-    const int total = 2 * TILE * CH;
+    const int total = TILES * TILE * CH;
     for (int c = threadIdx.x; c < total; c += NUM_THREADS) {
       const int lr = c / CH, ch = c % CH, r = row0 + lr;
       const bool in = r < rows;
@@ -324,7 +332,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     ptx::cp_async_commit();   // waited for below, under the key tiles' documents
   }
   // this softmax thread's row
-  const int t_own = warp >= 12 ? 1 : 0;
+  const int t_own = TILES == 2 && warp >= 12 ? 1 : 0;
   const int lr_own = (warp & 3) * 32 + lane + t_own * TILE;
   const int r_own = row0 + lr_own;
   const bool row_ok = warp >= 4 && r_own < rows;
@@ -345,7 +353,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   __syncthreads();
 
   // ---------------- key tiles of this CTA
-  const int row_last = min(row0 + 2 * TILE, rows) - 1;
+  const int row_last = min(row0 + TILES * TILE, rows) - 1;
   const int key_end = 1 + last_key(a, seq, (long)seq.start + row_last / a.G);
   const int jt_all = (key_end + TILE - 1) / TILE;
   const int jt0 = min(split * plan.tiles_per_split, jt_all);
@@ -381,7 +389,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         none = __any_sync(0xffffffffu, none);
         if (lane == 0 && jt < jt1) {
           uint8_t f = 0;
-          for (int t = 0; t < 2; ++t) {
+          for (int t = 0; t < TILES; ++t) {
             const RowTile& q = tiles[t];
             if (lo <= q.docs_hi && q.docs_lo <= hi) f |= 1u << (2 * t);
             if (!none && !q.any_none && lo == hi && q.docs_lo == q.docs_hi && lo == q.docs_lo) f |= 2u << (2 * t);
@@ -408,8 +416,8 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  // all columns are this CTA's, so they start at 0 (a constant the MMA operands are made of)
-  constexpr uint32_t tmem_base = 0;
+  // two row tiles have all columns, which start at 0 (a constant the MMA operands are made of)
+  const uint32_t tmem_base = TILES == 2 ? 0u : __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   // Row tile t takes the key tiles [jt0, end_t) that hold a document of its rows.
   auto end_of = [&](int t) {
@@ -417,13 +425,13 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     if (r_a >= rows) return 0;
     return min((1 + last_key(a, seq, (long)seq.start + r_b / a.G) + TILE - 1) / TILE, jt1);
   };
-  const int end0 = end_of(0), end1 = end_of(1);
+  const int end0 = end_of(0), end1 = TILES == 2 ? end_of(1) : 0;
   const int n_tiles = listed ? *list_len : jt1 - jt0;
   // entry n of the tiles to go through: key tile and the flags above
   auto entry = [&](int n) -> int { return listed ? list[n] : n << 4 | (docs ? 5 : 15); };
   auto takes = [&](int t, int e) -> bool { return jt0 + (e >> 4) < (t ? end1 : end0) && ((e >> (2 * t)) & 1); };
 
-  // registers: 640 x 96 at launch cover 128 x 32 + 512 x 112
+  // registers: 640 x 96 at launch cover 128 x 32 + 512 x 112, 384 x 80 cover 128 x 32 + 256 x 104
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0) {
@@ -459,7 +467,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           ptx::mbar_wait_bounded(full_bar(stage), phase, &never, WAIT_LIMIT_NS);
         }
       }
-    } else if (warp < 3) {
+    } else if (warp <= TILES) {
       // ---------------- MMA of row tile t: per key tile first P V of the tile before, then Q K^T,
       // which overwrites that P.  The tiles' MMAs come from two warps, so that neither waits
       // for the other's softmax, and from two schedulers: their issue slots are scarce beside
@@ -471,7 +479,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       const uint64_t d_k = ptx::smem_desc_sw128(sKV), d_v = desc_mn(sKV, C::HALF);
       const uint32_t k_hi = (uint32_t)(d_k >> 32), v_hi = (uint32_t)(d_v >> 32);
       const uint32_t q_lo = (uint32_t)ptx::smem_desc_sw128(sQ + t * C::Q_BYTES);
-      const uint32_t s_tmem = tmem_base + s_col(t), o_tmem = tmem_base + o_col<HD>(t);
+      const uint32_t s_tmem = tmem_base + s_col(t), o_tmem = tmem_base + o_col<HD, TILES>(t);
       int stage = 0, v_stage = 0, v_rows = TILE;
       uint32_t phase = 0, v_phase = 0, p_phase = 0, started = 0;
       bool ok = true, pend = false;
@@ -482,7 +490,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       auto p_ready = [&]() {   // the pending key tile's values and weights
         if (!wait(full_bar(v_stage), v_phase)) return;
         if (v_rows < TILE) {   // value rows past the last key: 0, whatever they hold
-          uint8_t* v = smem + 2 * C::Q_BYTES + v_stage * C::KV_BYTES;
+          uint8_t* v = smem + TILES * C::Q_BYTES + v_stage * C::KV_BYTES;
           const int n = (TILE - v_rows) * 8;
           for (int c = lane; c < n * (HD / 64); c += 32) {
             const int hf = c / n, e = c % n;
@@ -511,7 +519,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       // tiles' scores would come at the same time, and softmax and tensor cores would wait for
       // each other instead of working on one tile each.
       auto lock = [&]() {
-        if (lane == 0) {
+        if (TILES == 2 && lane == 0) {
           const uint64_t t0 = ptx::global_timer_ns();
           while (atomicCAS(mma_lock, 0, 1) != 0)
             if (*abort || ptx::global_timer_ns() - t0 > WAIT_LIMIT_NS) {
@@ -524,11 +532,11 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       };
       auto unlock = [&]() {
         __syncwarp();
-        if (lane == 0) atomicExch(mma_lock, 0);
+        if (TILES == 2 && lane == 0) atomicExch(mma_lock, 0);
       };
       for (int n = 0; n < n_tiles; ++n) {
         const int e = __shfl_sync(0xffffffffu, entry(n), 0), jt = jt0 + (e >> 4);
-        const bool mine = takes(t, e), other = takes(t ^ 1, e);
+        const bool mine = takes(t, e), other = TILES == 2 && takes(t ^ 1, e);
         if (!mine && !other) continue;
         const int k_stage = stage;
         const uint32_t k_phase = phase;
@@ -585,11 +593,14 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    if constexpr (TILES == 2)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---------------- softmax and output of row tile t_own
     const int t = t_own;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem_base + lane_addr + s_col(t), o_addr = tmem_base + lane_addr + o_col<HD>(t);
+    const uint32_t s_addr = tmem_base + lane_addr + s_col(t), o_addr = tmem_base + lane_addr + o_col<HD, TILES>(t);
     const int half = ((warp - 4) >> 2) & 1;            // keys 64 half .. of a tile, dims likewise
     constexpr int KH = TILE / 2, DH2 = HD / 2;
     const int lrow = (warp & 3) * 32 + lane;
@@ -633,7 +644,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
           for (int e = 0; e < KH; ++e) x[e] = a.scale < 0.f ? -x[e] : 0.f;
         }
-        float* xm = xch + ((phase * 2 + t) * 2) * TILE;
+        float* xm = xch + ((phase * TILES + t) * 2) * TILE;
         // the weights arg(score pair) of this half's 64 keys, in bf16 in the first 32 of their columns
         auto weights = [&](auto arg) {
           float2 sum = make_float2(0.f, 0.f);
@@ -840,7 +851,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(*tmem_slot, TMEM_COLS);
+    ptx::tmem_dealloc(*tmem_slot, C::COLS);
   }
 }
 
@@ -1924,9 +1935,43 @@ cudaError_t launch_maps(K kern, int threads, size_t smem, const ScoredAttention&
   return launch_kernel(kern, dim3((unsigned)grid), dim3(threads), smem, st, tk, tv, a, plan, err);
 }
 
+// The register counts that setmaxnreg moves between the warps are those of a launch with 96 (two
+// row tiles) or 80 registers a thread; with fewer the increase would never be granted, so a
+// build that came out otherwise is refused here.
+template <int HD, bool CAP, bool BIAS, int TILES>
+cudaError_t launch_rows_kernel(const ScoredAttention& a, const ScoredPlan& plan, DevError* err, cudaStream_t st) {
+  using C = Cfg<HD, TILES>;
+  struct One {   // a type of its own for each kernel
+    static bool ok() {
+      static std::atomic<int> state{0};
+      int s = state.load(std::memory_order_relaxed);
+      if (s == 0) {
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, scored_tc_kernel<HD, CAP, BIAS, TILES>) != cudaSuccess) {
+          cudaGetLastError();
+          return false;
+        }
+        s = at.numRegs == (TILES == 2 ? 96 : 80) ? 1 : 2;
+        state.store(s, std::memory_order_relaxed);
+      }
+      return s == 1;
+    }
+  };
+  if (!One::ok()) return cudaErrorInvalidConfiguration;
+  return launch_maps(scored_tc_kernel<HD, CAP, BIAS, TILES>, C::THREADS, C::SMEM, a, plan, err, st);
+}
+
+template <int HD, int TILES>
+cudaError_t launch_rows(const ScoredAttention& a, const ScoredPlan& plan, DevError* err, cudaStream_t st) {
+  if (a.cap > 0.f)
+    return a.slopes ? launch_rows_kernel<HD, true, true, TILES>(a, plan, err, st)
+                    : launch_rows_kernel<HD, true, false, TILES>(a, plan, err, st);
+  return a.slopes ? launch_rows_kernel<HD, false, true, TILES>(a, plan, err, st)
+                  : launch_rows_kernel<HD, false, false, TILES>(a, plan, err, st);
+}
+
 template <int HD>
 cudaError_t run_tc(const ScoredAttention& a, const ScoredPlan& plan, DevError* err, cudaStream_t st) {
-  const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
   cudaError_t e;
   if (plan.few == 16)
     e = launch_maps(scored_few_kernel<HD, 16>, F_THREADS, FewCfg<HD, 16>::SMEM, a, plan, err, st);
@@ -1934,12 +1979,10 @@ cudaError_t run_tc(const ScoredAttention& a, const ScoredPlan& plan, DevError* e
     e = launch_maps(scored_few_kernel<HD, 32>, F_THREADS, FewCfg<HD, 32>::SMEM, a, plan, err, st);
   else if (plan.few == 64)
     e = launch_maps(scored_few_kernel<HD, 64>, F_THREADS, FewCfg<HD, 64>::SMEM, a, plan, err, st);
-  else if (cap)
-    e = bias ? launch_maps(scored_tc_kernel<HD, true, true>, NUM_THREADS, Cfg<HD>::SMEM, a, plan, err, st)
-             : launch_maps(scored_tc_kernel<HD, true, false>, NUM_THREADS, Cfg<HD>::SMEM, a, plan, err, st);
+  else if (plan.tiles == 1)
+    e = launch_rows<HD, 1>(a, plan, err, st);
   else
-    e = bias ? launch_maps(scored_tc_kernel<HD, false, true>, NUM_THREADS, Cfg<HD>::SMEM, a, plan, err, st)
-             : launch_maps(scored_tc_kernel<HD, false, false>, NUM_THREADS, Cfg<HD>::SMEM, a, plan, err, st);
+    e = launch_rows<HD, 2>(a, plan, err, st);
   return e != cudaSuccess ? e : join<bf16, HD>(a, plan, st);
 }
 
@@ -1978,7 +2021,12 @@ ScoredPlan scored_attention_plan(const ScoredAttention& a, bool is_bf16, int num
   int block, tile, fill, least;
   if (is_bf16) {
     p.few = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
-    block = p.few ? p.few : 2 * TILE;
+    // One row tile a CTA, two CTAs an SM: their set-up, loads and last steps overlap, and short calls
+    // have twice the CTAs (16 heads x 4096: 145 us against 154 with two tiles, 4 x 8 heads x
+    // 512: 15 against 40).  With a cap, whose polynomial keeps the FMA units busy too, tiles in
+    // turn do better once they fill the SMs (16 heads x 4096: 176 us against 204).
+    p.tiles = a.cap > 0.f && (rows + 2 * TILE - 1) / (2 * TILE) * a.Hkv * a.B >= num_sms ? 2 : 1;
+    block = p.few ? p.few : p.tiles * TILE;
     tile = TILE;
     fill = p.few ? 4 : 1;
     least = 2;

@@ -184,6 +184,7 @@ struct ScoredConst {
 struct ScoredPlan {
   int splits = 1, tiles_per_split = 1, row_blocks = 1, parts = 1;
   int few = 0;   // rows of the kernel for few rows (0: not those)
+  int tiles = 2; // row tiles of a CTA of the kernel for many rows
   ScoredConst k;
   float* part_o = nullptr;
   float* part_lse = nullptr;
