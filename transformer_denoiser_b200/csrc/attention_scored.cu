@@ -20,7 +20,7 @@
 // heads x 8192 tokens).  Per key tile and row tile: S = Q K^T into 128 TMEM columns; the row's
 // threads read S, form p and write it in bf16 over S; O += P V with P as the TMEM operand.
 //
-// Few rows (scored_few_kernel, at most 64: new tokens over a cache): the keys take the MMA's
+// Few rows (scored_few_kernel, at most 16: new tokens over a cache): the keys take the MMA's
 // rows instead, S^T = K Q^T and O^T = V^T P^T, so that all four TMEM quarters, and with them
 // all softmax warps, share a key tile however few the queries are, and an MMA costs N = rows.
 //
@@ -860,6 +860,8 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 // At most NR query rows (all heads of a key head, all new tokens) against a range of keys:
 //   S^T [128 keys x NR] = K Q^T,  thread = key: scores, masks, p;  P [NR][128 keys] in shared
 //   memory;  O^T [dims x NR] += V^T P^T (V as an MN-major A operand, P K-major B).
+// NR = 16: with more rows their maxima, one redux each, cost more than the other kernel's 128 rows
+// (8 x 4 key heads, 40 rows over 8192 keys: 135 us against 35).
 // The row maxima cross the 128 threads by redux and shared memory; the row sums stay with the
 // threads until the end.  Bound by the K and V bytes.  Roles (192 threads): warp 0 TMA, warp
 // 1 MMA, warps 2-5 softmax and output.
@@ -870,14 +872,15 @@ struct FewCfg {
   static constexpr uint32_t P_BYTES = NR * 256;
   static constexpr uint32_t KV_BYTES = TILE * HD * 2;
   static constexpr uint32_t HALF = TILE * 128;
-  // 16 rows: two CTAs an SM, so that one's set-up and last tiles run under the other's loads
-  static constexpr int NST = NR == 16 ? (HD == 128 ? 3 : 6) : (HD == 128 ? 5 : 10);
+  // two CTAs an SM, so that one's set-up and last tiles run under the other's loads
+  static constexpr int NST = HD == 128 ? 3 : 6;
   static constexpr size_t BODY = Q_BYTES + P_BYTES + (size_t)NST * KV_BYTES;
   // rows' last key, position, document, slope; maxima (2 x 4 warps), references and factors (4 warps)
   static constexpr size_t ROWS = NR * 4 * (4 + 8 + 8 + 1);
   static constexpr size_t SMEM = 1024 + BODY + ROWS + (2 * NST + 8) * 8 + 16;
-  static constexpr uint32_t COLS = 3 * NR <= 64 ? 64 : 3 * NR <= 128 ? 128 : 256;
-  static_assert(SMEM <= 232448, "shared memory");
+  static constexpr uint32_t COLS = 64;
+  static_assert(NR == 16, "one TMEM load a thread, 3 * NR columns");
+  static_assert(SMEM <= 232448 / 2 - 1024, "shared memory of two CTAs");
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -887,7 +890,7 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 template <int HD, int NR>
-__global__ void __launch_bounds__(F_THREADS, NR == 16 ? 2 : 1)
+__global__ void __launch_bounds__(F_THREADS, 2)
 scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ ScoredAttention a, const __grid_constant__ ScoredPlan plan,
                   DevError* err) {
@@ -1096,11 +1099,6 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       float x[NR];
       const uint32_t s_addr = tmem_base + lane_addr + (n & 1) * NR;
       ptx::tmem_ld16_at<0>(s_addr, x);
-      if constexpr (NR > 16) ptx::tmem_ld16_at<NR - 16>(s_addr + NR - 16, x);
-      if constexpr (NR > 32) {
-        ptx::tmem_ld16_at<16>(s_addr + 16, x);
-        ptx::tmem_ld16_at<NR - 32>(s_addr + NR - 32, x);
-      }
       ptx::tmem_ld_wait();
       if (cap) {
         cap_scores(cc, x);
@@ -1909,12 +1907,69 @@ __global__ void __launch_bounds__(128) scored_join_kernel(const __grid_constant_
   if (!__all_sync(0xffffffffu, finite)) row_by_warp<T, HD>(a, b, hq, i);
 }
 
+// The same with one warp a row, for few parts: all of them in flight at once.
+constexpr int JOIN_WARP_PARTS = 8;
+template <typename T, int HD>
+__global__ void __launch_bounds__(128) scored_join_warp_kernel(const __grid_constant__ ScoredAttention a,
+                                                               const __grid_constant__ ScoredPlan plan) {
+  constexpr int PER = HD / 32;
+  ptx::pdl_wait();
+  ptx::pdl_trigger();
+  const int rows = a.Sq * a.G, lane = threadIdx.x & 31;
+  const long n_rows = (long)a.B * a.Hkv * rows, r = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (r >= n_rows) return;
+  const float mine = lane < plan.parts ? plan.part_lse[lane * n_rows + r] : -INFINITY;
+  float top = mine;
+#pragma unroll
+  for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top = __shfl_sync(0xffffffffu, top, 0);
+  const float w_mine = exp2f(mine - (top == -INFINITY ? 0.f : top));
+  float w[JOIN_WARP_PARTS], v[JOIN_WARP_PARTS][PER], total = 0.f, y[PER];
+#pragma unroll
+  for (int s = 0; s < JOIN_WARP_PARTS; ++s) {
+    w[s] = __shfl_sync(0xffffffffu, w_mine, s);
+    const float* po = plan.part_o + (s * n_rows + r) * HD + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) v[s][e] = 0.f;
+    if (s < plan.parts && w[s] != 0.f) {   // a part that saw nothing has no values
+      if constexpr (PER == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(po);
+        v[s][0] = t.x; v[s][1] = t.y; v[s][2] = t.z; v[s][3] = t.w;
+      } else {
+        const float2 t = *reinterpret_cast<const float2*>(po);
+        v[s][0] = t.x; v[s][1] = t.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) y[e] = 0.f;
+#pragma unroll
+  for (int s = 0; s < JOIN_WARP_PARTS; ++s) {
+    if (s < plan.parts) total += w[s];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) y[e] = fmaf(s < plan.parts ? w[s] : 0.f, v[s][e], y[e]);
+  }
+  const int rr = (int)(r % rows), i = rr / a.G, g = rr - i * a.G;
+  const int bh = (int)(r / rows), hk = bh % a.Hkv, b = bh / a.Hkv, hq = hk * a.G + g;
+  T* out = static_cast<T*>(a.out) + b * a.o_batch + i * a.o_token + hq * a.o_head + lane * PER;
+  bool finite = true;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    y[e] = total == 0.f ? 0.f : y[e] / total;
+    finite = finite && fabsf(y[e]) < INFINITY;
+    out[e] = from_f<T>(y[e]);
+  }
+  if (!__all_sync(0xffffffffu, finite)) row_by_warp<T, HD>(a, b, hq, i);
+}
+
 // ---------------------------------------------------------------- host side
 
 template <typename T, int HD>
 cudaError_t join(const ScoredAttention& a, const ScoredPlan& plan, cudaStream_t st) {
   if (plan.parts == 1) return cudaSuccess;
   const long n_rows = (long)a.B * a.Hq * a.Sq;
+  if (plan.parts <= JOIN_WARP_PARTS)
+    return launch_kernel(scored_join_warp_kernel<T, HD>, dim3((unsigned)((n_rows + 3) / 4)), dim3(128), 0, st, a, plan);
   return launch_kernel(scored_join_kernel<T, HD>, dim3((unsigned)n_rows), dim3(128), 0, st, a, plan);
 }
 
@@ -1973,12 +2028,8 @@ cudaError_t launch_rows(const ScoredAttention& a, const ScoredPlan& plan, DevErr
 template <int HD>
 cudaError_t run_tc(const ScoredAttention& a, const ScoredPlan& plan, DevError* err, cudaStream_t st) {
   cudaError_t e;
-  if (plan.few == 16)
+  if (plan.few)
     e = launch_maps(scored_few_kernel<HD, 16>, F_THREADS, FewCfg<HD, 16>::SMEM, a, plan, err, st);
-  else if (plan.few == 32)
-    e = launch_maps(scored_few_kernel<HD, 32>, F_THREADS, FewCfg<HD, 32>::SMEM, a, plan, err, st);
-  else if (plan.few == 64)
-    e = launch_maps(scored_few_kernel<HD, 64>, F_THREADS, FewCfg<HD, 64>::SMEM, a, plan, err, st);
   else if (plan.tiles == 1)
     e = launch_rows<HD, 1>(a, plan, err, st);
   else
@@ -2013,41 +2064,63 @@ cudaError_t launch_f32(const ScoredAttention& a, const ScoredPlan& plan, cudaStr
 }  // namespace
 
 // How a call is laid out over the GPU: row blocks by the number of rows a key head has, and
-// keys split while the CTAs do not fill the SMs (`fill` CTAs an SM) and every part keeps
-// `least` key tiles.
+// keys split where that takes less time by this estimate (us): the CTAs in turn on the slots
+// of all SMs, each `start` and `step` a key tile, and the join its launch, a little for each
+// part and the parts written and read again.  (32 x 8 key heads over 2000 keys, one token: one
+// part 47 us, two 56; 4 x 8 heads x 100 rows over 2000 keys: one part 37 us, eight 21; 4 x 8
+// heads x 512 tokens: one part 15 us, two 24.)
 ScoredPlan scored_attention_plan(const ScoredAttention& a, bool is_bf16, int num_sms) {
   ScoredPlan p;
   const long rows = (long)a.Sq * a.G;
-  int block, tile, fill, least;
-  if (is_bf16) {
-    p.few = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
+  const bool wide = a.HD == 128;
+  int block, tile, slots;
+  double start, step;
+  p.few = rows <= 16 ? 16 : 0;
+  if (p.few) {
+    block = 16;
+    tile = is_bf16 ? TILE : FT;
+    slots = 2 * num_sms;
+    start = 4;
+    step = wide ? 2.9 : 1.5;   // 64 KB of keys and values (128 dims) at two CTAs' share of the bandwidth
+  } else if (is_bf16) {
     // One row tile a CTA, two CTAs an SM: their set-up, loads and last steps overlap, and short calls
     // have twice the CTAs (16 heads x 4096: 145 us against 154 with two tiles, 4 x 8 heads x
     // 512: 15 against 40).  With a cap, whose polynomial keeps the FMA units busy too, tiles in
     // turn do better once they fill the SMs (16 heads x 4096: 176 us against 204).
     p.tiles = a.cap > 0.f && (rows + 2 * TILE - 1) / (2 * TILE) * a.Hkv * a.B >= num_sms ? 2 : 1;
-    block = p.few ? p.few : p.tiles * TILE;
+    block = p.tiles * TILE;
     tile = TILE;
-    fill = p.few ? 4 : 1;
-    least = 2;
+    slots = p.tiles == 1 ? 2 * num_sms : num_sms;
+    start = 6;
+    step = wide ? 2.0 : 1.5;
   } else {
-    p.few = rows <= 16 ? 16 : 0;
-    block = p.few ? 16 : TILE;
-    tile = 64;
-    fill = p.few ? 2 : 1;
-    least = 2;
+    block = TILE;
+    tile = S3_KEYS;
+    slots = num_sms;
+    start = 12;
+    step = wide ? 4.0 : 2.5;
   }
   p.k = scored_const(a.scale, a.cap);
   p.row_blocks = (int)((rows + block - 1) / block);
   const int key_tiles = (a.Sk + tile - 1) / tile;
-  const long ctas = (long)p.row_blocks * a.Hkv * a.B, want = (long)fill * num_sms;
-  long splits = ctas < want ? want / ctas : 1;
-  if (splits > key_tiles / least) splits = key_tiles / least;
-  if (splits < 1) splits = 1;
-  p.tiles_per_split = (int)((key_tiles + splits - 1) / splits);
-  if (p.tiles_per_split < 1) p.tiles_per_split = 1;
-  p.splits = key_tiles > 0 ? (key_tiles + p.tiles_per_split - 1) / p.tiles_per_split : 1;
-  p.parts = p.splits;
+  const double ctas = (double)p.row_blocks * a.Hkv * a.B;
+  const double part_mb = (double)a.B * a.Hq * a.Sq * a.HD * 4e-6;
+  double least = 1e30;
+  for (int rounds = 0; rounds <= 4; ++rounds) {   // one part, or as many as fill 1 to 4 rounds of CTAs
+    long s = rounds == 0 ? 1 : (long)(rounds * slots / ctas);
+    if (s > key_tiles / 2) s = key_tiles / 2;
+    if (s < 1 || (rounds > 0 && s == 1) || (s > 1 && s * part_mb > 256)) continue;
+    const int per = key_tiles > 0 ? (int)((key_tiles + s - 1) / s) : 1;
+    const int parts = key_tiles > 0 ? (key_tiles + per - 1) / per : 1;
+    // (a last round that is partly filled takes part of a round's time)
+    const double w = ctas * parts / slots, waves = w <= 1 ? 1 : (w + ceil(w)) / 2;
+    const double us = waves * (start + per * step) + (parts > 1 ? 3 + 0.1 * parts + parts * part_mb * 2 / 3 : 0);
+    if (us < least) {
+      least = us;
+      p.tiles_per_split = per;
+      p.splits = p.parts = parts;
+    }
+  }
   p.bytes = p.parts > 1 ? (size_t)p.parts * a.B * a.Hkv * rows * (a.HD + 1) * 4 : 0;
   return p;
 }
