@@ -169,7 +169,10 @@ KIMODO_API int kimodo_gemm_int8(const void* A, long long lda, const float* a_sca
  *   consecutive.  Strides (elements) of batch, token and head: multiples of 16 bytes, at
  *   least head_dim; that of an extent of one is ignored.  Bases 16-byte aligned.  out must
  *   not overlap the inputs.
- * dtype: KIMODO_BF16 (tcgen05 tensor cores; fp32 scores, softmax and sums) or KIMODO_FP32.
+ * dtype: KIMODO_BF16 (tcgen05 tensor cores; fp32 scores, softmax and sums, weights rounded to
+ *   bf16) or KIMODO_FP32 (fp32 throughout; above 16 rows per key head, q_len x q_heads /
+ *   kv_heads, products run on the tensor cores with every operand in three bf16 parts, 24
+ *   bits as fp32 has, and are summed in fp32).
  * slopes: fp32 [q_heads].  prefix (with causal), kv_lengths, q_start: int32 [batch];
  *   q_documents int32 [batch, q_len], kv_documents int32 [batch, kv_len] (both or
  *   neither).  NULL switches an option off; kv_lengths NULL: kv_len (lengths are clamped to

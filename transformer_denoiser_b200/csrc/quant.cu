@@ -86,7 +86,7 @@ __device__ __forceinline__ void row_reduce(float& s, uint32_t& m, float* xs, uin
 }
 
 template <typename TX, typename TR, bool NORM, int TPR, int NG, bool VEC>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, NORM && TPR == 256 ? 5 : NORM && TPR == 64 ? 20 : 1) rows_int8_kernel(RowsInt8 a) {
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, NORM && TPR == 256 ? 5 : NORM && TPR == 64 ? 20 : !NORM && TPR == 128 ? 8 : 1) rows_int8_kernel(RowsInt8 a) {
   constexpr bool RES = Elem<TR>::size != 0;
   __shared__ float xs[TPR / 32];
   __shared__ uint32_t xm[TPR / 32];
