@@ -115,6 +115,8 @@ def test_rows_that_see_nothing(Sq, Sk, dtype):
 def test_no_keys(dtype):
     q, k, v = _qkv(1, 2, 5, 0, 4, 2, 64, dtype)
     assert (kb.attention_scored(q, k, v) == 0).all()
+    d = torch.zeros(2, 5, dtype=torch.int32).cuda()
+    assert (kb.attention_scored(q, k, v, q_documents=d, kv_documents=d[:, :0].contiguous(), causal=True) == 0).all()
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])

@@ -106,6 +106,15 @@ def test_attention_scored_refusals(lib, change, text):
     assert n.value == 0
 
 
+def test_documents_without_keys_are_not_refused(lib):
+    """A tensor of no elements has no address: with kv_len 0, kv_documents may be NULL."""
+    a, n = _args(kv_len=0, k=None, v=None, q_documents=P), ctypes.c_size_t(77)
+    rc = lib.kimodo_attention_scored_workspace(ctypes.byref(a), ctypes.byref(n))
+    assert rc == (0 if torch.cuda.is_available() else -4), lib.kimodo_last_error()
+    _refused(lib, lib.kimodo_attention_scored_workspace(ctypes.byref(_args(kv_len=0, kv_documents=P)), ctypes.byref(n)),
+             b"come together")
+
+
 def test_attention_scored_null_arguments(lib):
     _refused(lib, lib.kimodo_attention_scored(None, None, 0, None), b"arguments are NULL")
     _refused(lib, lib.kimodo_attention_scored_workspace(ctypes.byref(_args()), None), b"bytes is NULL")

@@ -172,7 +172,8 @@ int scored_args(const kimodo_scored_attention* p, ScoredAttention* a) {
   if (p->cap > 0.f && !(fabsf(p->scale) <= 1e6f * p->cap))
     return set_error(KIMODO_EINVAL, "cap must be at least a millionth of the scale");
   if (p->prefix && !p->causal) return set_error(KIMODO_EINVAL, "prefix needs causal");
-  if ((p->q_documents == nullptr) != (p->kv_documents == nullptr))
+  // (without keys there are no documents of keys, whose tensor of no elements has no address)
+  if ((p->q_documents == nullptr) != (p->kv_documents == nullptr) && (p->kv_len > 0 || !p->q_documents))
     return set_error(KIMODO_EINVAL, "q_documents and kv_documents come together");
   // strides: an extent of one has none; 16-byte rows (vector loads, TMA)
   const int unit = p->dtype == KIMODO_BF16 ? 8 : 4;
@@ -197,7 +198,9 @@ int scored_args(const kimodo_scored_attention* p, ScoredAttention* a) {
       misaligned(p->kv_documents, 4) || misaligned(p->kv_lengths, 4) || misaligned(p->q_start, 4))
     return set_error(KIMODO_EINVAL, "slopes and index tensors must be aligned to their elements");
   a->q = p->q; a->k = p->k; a->v = p->v; a->out = p->out;
-  a->slopes = p->slopes; a->prefix = p->prefix; a->q_doc = p->q_documents; a->kv_doc = p->kv_documents;
+  a->slopes = p->slopes; a->prefix = p->prefix;
+  a->q_doc = p->kv_len > 0 ? p->q_documents : nullptr;
+  a->kv_doc = p->kv_len > 0 ? p->kv_documents : nullptr;
   a->kv_lengths = p->kv_lengths; a->q_start = p->q_start;
   a->q_batch = s[0][0]; a->q_token = s[0][1]; a->q_head = s[0][2];
   a->k_batch = s[1][0]; a->k_token = s[1][1]; a->k_head = s[1][2];
