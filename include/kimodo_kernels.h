@@ -117,6 +117,7 @@ KIMODO_API int kimodo_global_to_local_root(const float* root, const float* x, co
  * x: fp32 (x_bf16 = 0) or bf16 (1) [rows, cols], row stride ldx elements.  q: int8, row
  * stride ldq.  scale: fp32 [rows].  1 <= rows, 1 <= cols <= 32768.  Rows on 16-byte
  * boundaries (8 for q) with cols a multiple of 8 take the faster path; none is required.
+ * q must not overlap x.
  */
 KIMODO_API int kimodo_quantize_int8(const void* x, long long ldx, int x_bf16, void* q, long long ldq,
                                     float* scale, int rows, int cols, void* stream);
@@ -128,7 +129,7 @@ KIMODO_API int kimodo_quantize_int8(const void* x, long long ldx, int x_bf16, vo
  * t is taken from the fp32 sum, not from the rounded resid_out.
  * x as above; resid, resid_out: fp32 (resid_bf16 = 0) or bf16 (1), strides ldr, ldro; both
  * or neither; resid_out may equal resid (in place, same stride) but not overlap it or x
- * otherwise.  gamma: fp32 [cols].  eps: finite, >= 0.
+ * otherwise; q overlaps none of them.  gamma: fp32 [cols].  eps: finite, >= 0.
  */
 KIMODO_API int kimodo_rms_norm_int8(const void* x, long long ldx, int x_bf16, const void* resid, long long ldr,
                                     void* resid_out, long long ldro, int resid_bf16, const float* gamma, float eps,
@@ -144,7 +145,8 @@ KIMODO_API int kimodo_rms_norm_int8(const void* x, long long ldx, int x_bf16, co
  * a_scale: fp32 [M]; w_scale: fp32 [N]; bias: fp32 [N] or NULL.
  * epilogue: KIMODO_EPI_*; resid fp32 [M, ldr] with KIMODO_EPI_BIAS_RESID (may equal out),
  * ignored otherwise.  out: bf16 (out_f32 = 0) or fp32 (1), row stride ldo, no alignment
- * beyond its elements; GELU and SiLU write bf16, the residual epilogue fp32.
+ * beyond its elements; GELU and SiLU write bf16, the residual epilogue fp32.  out must not
+ * overlap A or W, nor resid unless it equals it (in place, same stride).
  */
 #define KIMODO_INT8_MAX_K 131071
 KIMODO_API int kimodo_gemm_int8(const void* A, long long lda, const float* a_scale, const void* W, long long ldw,

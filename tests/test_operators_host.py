@@ -77,6 +77,20 @@ def test_gemm_int8_refusals(lib):
     _refused(lib, call(bias=P + 2), b"aligned to their elements")
 
 
+def test_outputs_that_start_on_an_input_are_refused(lib):
+    word = b"must not overlap the inputs"
+    _refused(lib, lib.kimodo_quantize_int8(P, 8, 0, P, 8, 2 * P, 1, 8, None), word)
+    for x, r, ro, q in ((P, 2 * P, P, 3 * P), (P, 2 * P, 3 * P, P), (P, 2 * P, 3 * P, 2 * P), (P, 2 * P, 3 * P, 3 * P),
+                        (P, 2 * P, 2 * P, 2 * P)):
+        _refused(lib, lib.kimodo_rms_norm_int8(x, 8, 0, r, 8, ro, 8, 0, 4 * P, 1e-6, q, 8, 5 * P, 1, 8, None), word)
+    for out in (P, 2 * P):
+        _refused(lib, lib.kimodo_gemm_int8(P, 64, 3 * P, 2 * P, 64, 4 * P, None, None, 0, out, 8, 1, 8, 64, 0, 0, None),
+                 word)
+    for out in (P, 2 * P, 3 * P):
+        a = _args(q=P, k=2 * P, v=3 * P, out=out)
+        _refused(lib, lib.kimodo_attention_scored(ctypes.byref(a), None, 0, None), word)
+
+
 def _args(**change):
     a = kb.ScoredAttention(P, P, P, P, None, None, None, None, None, None, (512, 64, 64), (512, 64, 64), (512, 64, 64),
                            (512, 64, 64), 2, 8, 8, 1, 1, 64, kb.BF16, 0, 0.125, 0.0)

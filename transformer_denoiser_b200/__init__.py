@@ -339,7 +339,7 @@ def quantize_int8(x):
 def rms_norm_int8(x, gamma, residual=None, eps=1e-6, residual_out=None):
     """(q, scale, residual_out): int8 rows and fp32 scales of the RMS norm of x + residual times
     gamma (fp32 [cols]), and the sum in the residual's type (None without a residual).
-    x and residual [rows, cols], fp32 or bf16; residual_out may be residual itself."""
+    x and residual [rows, cols], fp32 or bf16; residual_out may be residual itself, not x."""
     lib = _lib or load_library()
     T = _T or _use_torch()
     dev = _device_of(x, "x")
@@ -373,7 +373,7 @@ def rms_norm_int8(x, gamma, residual=None, eps=1e-6, residual_out=None):
 def gemm_int8(a, a_scale, w, w_scale, bias=None, epilogue=EPI_BIAS, out_f32=False, resid=None, out=None):
     """out = epilogue(a_scale[:, None] * w_scale * (a w^T) + bias): int8 a [M, K], w [N, K] (rows on
     16-byte boundaries), fp32 scales [M], [N] and bias [N] or None; out bf16 or fp32 [M, N];
-    resid fp32 [M, N] with EPI_BIAS_RESID (may be out)."""
+    resid fp32 [M, N] with EPI_BIAS_RESID (may be out, which overlaps no other input)."""
     lib = _lib or load_library()
     T = _T or _use_torch()
     dev = _device_of(a, "a")
@@ -417,7 +417,7 @@ def attention_scored(q, k, v, scale=None, cap=0.0, slopes=None, causal=False, pr
     fp32 [Hq]: minus slope * |position distance|; causal, with prefix int32 [B] keys seen by
     all; documents int32 [B, Sq], [B, Sk]: only equal numbers >= 0 meet; kv_lengths int32
     [B]; q_start int32 [B]: position of the first query (default Sk - Sq).  A query that sees
-    no key gets 0.  Returns [B, Sq, Hq, D]."""
+    no key gets 0.  out must not overlap the inputs.  Returns [B, Sq, Hq, D]."""
     lib = _lib or load_library()
     T = _T or _use_torch()
     dev = _device_of(q, "q")

@@ -70,6 +70,14 @@ int check_type(const char* what, const void* p, int bf16_flag) {
   return KIMODO_OK;
 }
 
+// An output that starts where an input does: rows would be overwritten that other threads, or
+// the same call again (attention's rows with non-finite results), still read.
+int check_apart(const char* what, const void* out, std::initializer_list<const void*> inputs) {
+  for (const void* p : inputs)
+    if (p != nullptr && p == out) return set_error(KIMODO_EINVAL, "%s must not overlap the inputs", what);
+  return KIMODO_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -80,6 +88,7 @@ int kimodo_quantize_int8(const void* x, long long ldx, int x_bf16, void* q, long
   KD_TRY(check_rows(x, ldx, q, ldq, scale, rows, cols));
   KD_TRY(check_type("x", x, x_bf16));
   if (misaligned(scale, 4)) return set_error(KIMODO_EINVAL, "scale is not aligned to its elements");
+  KD_TRY(check_apart("q", q, {x}));
   KD_TRY(check_here({x, q, scale}));
   RowsInt8 a;
   a.x = x; a.ldx = ldx; a.q = static_cast<int8_t*>(q); a.ldq = ldq; a.scale = scale; a.rows = rows; a.cols = cols;
@@ -105,6 +114,8 @@ int kimodo_rms_norm_int8(const void* x, long long ldx, int x_bf16, const void* r
   }
   if (misaligned(scale, 4) || misaligned(gamma, 4))
     return set_error(KIMODO_EINVAL, "gamma and scale must be aligned to their elements");
+  KD_TRY(check_apart("resid_out", resid_out, {x}));
+  KD_TRY(check_apart("q", q, {x, resid, resid_out}));
   KD_TRY(check_here({x, resid, resid_out, gamma, q, scale}));
   RowsInt8 a;
   a.x = x; a.ldx = ldx; a.r_in = resid; a.ldr_in = ldr; a.r_out = resid_out; a.ldr_out = ldro; a.gamma = gamma;
@@ -136,6 +147,7 @@ int kimodo_gemm_int8(const void* A, long long lda, const float* a_scale, const v
   if (misaligned(out, out_f32 ? 4 : 2) || misaligned(a_scale, 4) || misaligned(w_scale, 4) || misaligned(bias, 4) ||
       misaligned(resid, 4))
     return set_error(KIMODO_EINVAL, "out, resid, bias and scales must be aligned to their elements");
+  KD_TRY(check_apart("out", out, {A, W}));
   if (!gemm_tc_available()) return set_error(KIMODO_EUNSUPPORTED, "cuTensorMapEncodeTiled is unavailable");
   KD_TRY(check_here({A, a_scale, W, w_scale, bias, epilogue == KIMODO_EPI_BIAS_RESID ? resid : nullptr, out}));
   const int sms = current_sms();
@@ -233,6 +245,7 @@ int kimodo_attention_scored(const kimodo_scored_attention* args, void* workspace
   clear_error();
   ScoredAttention a;
   KD_TRY(scored_args(args, &a));
+  KD_TRY(check_apart("out", a.out, {a.q, a.k, a.v}));
   KD_TRY(check_here({a.q, a.k, a.v, a.out, a.slopes, a.prefix, a.q_doc, a.kv_doc, a.kv_lengths, a.q_start}));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = args->dtype == KIMODO_BF16;
