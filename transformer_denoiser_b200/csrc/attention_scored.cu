@@ -13,12 +13,12 @@
 //
 // Many rows (scored_tc_kernel): an SM works on two tiles of 128 rows, as two CTAs or as one that
 // takes both in turn; while the softmax of one runs, the tensor cores work on the other.
-// Roles (128 threads and 256 a row tile): warp 0 TMA of K and
-// V tiles (128 keys, 128-byte swizzle), warps 1 and 2 MMA issue of tile 0 and 1, warps 4-11 and 12-19 softmax and
-// output of tile 0 and 1, two threads a row, each half of the keys (one thread a row left the
-// four schedulers two warps each, too few to hide the latencies: 490 against 431 us for 16
-// heads x 8192 tokens).  Per key tile and row tile: S = Q K^T into 128 TMEM columns; the row's
-// threads read S, form p and write it in bf16 over S; O += P V with P as the TMEM operand.
+// Roles (128 threads and 256 a row tile): warp 0 TMA of K and V tiles (128 keys, 128-byte
+// swizzle), warps 1 and 2 MMA issue of tile 0 and 1, warps 4-11 and 12-19 softmax and output
+// of tile 0 and 1, two threads a row, each half of the keys (one thread a row left the four
+// schedulers two warps each, too few to hide the latencies: 490 against 431 us for 16 heads x
+// 8192 tokens).  Per key tile and row tile: S = Q K^T into 128 TMEM columns; the row's threads
+// read S, form p and write it in bf16 over S; O += P V with P as the TMEM operand.
 //
 // Few rows (scored_few_kernel, at most 16: new tokens over a cache): the keys take the MMA's
 // rows instead, S^T = K Q^T and O^T = V^T P^T, so that all four TMEM quarters, and with them
@@ -494,7 +494,8 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           const int n = (TILE - v_rows) * 8;
           for (int c = lane; c < n * (HD / 64); c += 32) {
             const int hf = c / n, e = c % n;
-            *reinterpret_cast<uint4*>(v + hf * C::HALF + (v_rows + e / 8) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(v + hf * C::HALF + (v_rows + e / 8) * 128 + (e & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
@@ -1043,7 +1044,8 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         const int cnt = (TILE - v_rows) * 8;
         for (int c = lane; c < cnt * (HD / 64); c += 32) {
           const int hf = c / cnt, e = c % cnt;
-          *reinterpret_cast<uint4*>(v + hf * C::HALF + (v_rows + e / 8) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(v + hf * C::HALF + (v_rows + e / 8) * 128 + (e & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -1270,7 +1272,8 @@ template <int HD>
 __global__ void __launch_bounds__(NT, 2) scored_f32_kernel(const __grid_constant__ ScoredAttention a,
                                                             const __grid_constant__ ScoredPlan plan) {
   using C = F32Cfg<HD>;
-  constexpr int CG = C::CG, RG = C::RG, BM = C::BM, LD = C::LD, LP = C::LP, ND = HD / (4 * CG);   // float4 of outputs per row and thread
+  constexpr int CG = C::CG, RG = C::RG, BM = C::BM, LD = C::LD, LP = C::LP;
+  constexpr int ND = HD / (4 * CG);   // float4 of outputs per row and thread
   extern __shared__ float fsm[];
   float* sQ = fsm;
   float* sK = sQ + BM * LD;
@@ -1806,8 +1809,9 @@ scored_split3_kernel(const __grid_constant__ ScoredAttention a, const __grid_con
     const bool seen = n_tiles > 0 && l != 0.f;   // l is NaN where a score is
     bool finite = true;
     const long n_rows = (long)a.B * a.Hkv * rows, prow = ((long)b * a.Hkv + hk) * rows + r_own;
-    float* o = plan.parts == 1 ? static_cast<float*>(a.out) + b * a.o_batch + i_own * a.o_token + (long)(hk * a.G + g_own) * a.o_head
-                               : plan.part_o + ((long)split * n_rows + prow) * HD;
+    float* o = plan.part_o + ((long)split * n_rows + prow) * HD;
+    if (plan.parts == 1)
+      o = static_cast<float*>(a.out) + b * a.o_batch + i_own * a.o_token + (long)(hk * a.G + g_own) * a.o_head;
     const bool write = ok && row_ok && (plan.parts == 1 || seen);
     const float inv = 1.f / l;
 #pragma unroll 1

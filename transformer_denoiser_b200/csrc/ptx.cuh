@@ -342,17 +342,7 @@ __device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
-// ---------------------------------------------------------------- A operand and stores in TMEM
-// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs (A: 2 values a column), fp32 accumulate.
-__device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
+// ---------------------------------------------------------------- stores to TMEM
 // 32 lanes x 32 bits, 16 consecutive columns per thread.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -376,8 +366,8 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(leader));
   return leader != 0;
 }
-// tc_mma_bf16 / tc_mma_bf16_ta with descriptors as (low, high) words: the low word holds the
-// address, so a step along K is one 32-bit addition.
+// tc_mma_bf16 with descriptors as (low, high) words: the low word holds the address, so a step
+// along K is one 32-bit addition.
 __device__ __forceinline__ void tc_mma_bf16_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
                                                uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -389,6 +379,7 @@ __device__ __forceinline__ void tc_mma_bf16_lo(uint32_t d_tmem, uint32_t a_lo, u
       ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs (A: 2 values a column), fp32 accumulate.
 __device__ __forceinline__ void tc_mma_bf16_ta_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
                                                   uint32_t idesc, uint32_t accumulate) {
   asm volatile(

@@ -85,8 +85,13 @@ __device__ __forceinline__ void row_reduce(float& s, uint32_t& m, float* xs, uin
   }
 }
 
+// Rows in flight hide the latency of their one pass, so registers are held down where the
+// compiler would take more than these CTAs an SM leave (norm of 8192 x 4096: 59 -> 49 us;
+// quantisation of 12289 x 2731 fp32: 41 -> 38 us).
+constexpr int ctas_per_sm(bool norm, int tpr) { return norm ? (tpr == 256 ? 5 : tpr == 64 ? 20 : 1) : tpr == 128 ? 8 : 1; }
+
 template <typename TX, typename TR, bool NORM, int TPR, int NG, bool VEC>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, NORM && TPR == 256 ? 5 : NORM && TPR == 64 ? 20 : !NORM && TPR == 128 ? 8 : 1) rows_int8_kernel(RowsInt8 a) {
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, ctas_per_sm(NORM, TPR)) rows_int8_kernel(RowsInt8 a) {
   constexpr bool RES = Elem<TR>::size != 0;
   __shared__ float xs[TPR / 32];
   __shared__ uint32_t xm[TPR / 32];
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, NORM && TPR == 256 ? 5 
         }
       ht = 0;
       row_reduce<TPR>(hs, ht, xs, xm);
-      scale = amax / hm / (127.f * sqrtf(hs / (float)cols));   // NaN where a value is not finite
+      scale = amax / hm / (127.f * sqrtf(hs / (float)cols + a.eps / hm / hm));   // NaN where a value is not finite
     }
   }
   if (t == 0) a.scale[row] = !finite ? __uint_as_float(0x7fc00000u) : top == 0 ? 0.f : scale;
