@@ -126,7 +126,8 @@ KIMODO_API int kimodo_quantize_int8(const void* x, long long ldx, int x_bf16, vo
  * RMS norm with the residual's addition, its output in 8-bit integers:
  *   h = x + resid (fp32; resid NULL: h = x), resid_out = h in the residual's type,
  *   t = h gamma / sqrt(mean_c h^2 + eps), q and scale as kimodo_quantize_int8 of t.
- * t is taken from the fp32 sum, not from the rounded resid_out.
+ * t is taken from the fp32 sum, not from the rounded resid_out.  A row in which an h or an
+ * h gamma leaves fp32's range has q = 0 and scale NaN.
  * x as above; resid, resid_out: fp32 (resid_bf16 = 0) or bf16 (1), strides ldr, ldro; both
  * or neither; resid_out may equal resid (in place, same stride) but not overlap it or x
  * otherwise; q overlaps none of them.  gamma: fp32 [cols].  eps: finite, >= 0.

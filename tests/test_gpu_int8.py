@@ -116,6 +116,16 @@ def test_rms_norm_int8_extreme_magnitudes(scale):
     _check_norm(x, None, gamma, 1e-6, q, s, None, scale)
 
 
+@pytest.mark.parametrize("cols", [512, 333])
+@pytest.mark.parametrize("scale,eps", [(1e-25, 0.0), (1e-20, 1e-38), (1e-32, 0.0), (1e-17, 1e-36), (1e-36, 1e-33)])
+def test_rms_norm_int8_tiny_rows_without_eps(scale, eps, cols):
+    """Squares that underflow and an eps that does not hide it."""
+    x, _, gamma = _norm_case(4, cols, torch.float32, None, 13, scale)
+    eps = float(torch.tensor(eps))   # the value that the call takes
+    q, s, _ = kb.rms_norm_int8(x.cuda(), gamma.cuda(), None, eps)
+    _check_norm(x, None, gamma, eps, q, s, None, (scale, eps))
+
+
 def test_rms_norm_int8_zero_and_nonfinite_rows():
     x, _, gamma = _norm_case(5, 300, torch.float32, None, 12)
     x[0] = 0

@@ -168,10 +168,12 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, ctas_per_sm(NORM, TPR))
   const float amax = __uint_as_float(top);
   float scale = amax / 127.f;
   if constexpr (NORM) {
-    if (s < INFINITY) {
-      scale = amax / (127.f * sqrtf(s / (float)cols + a.eps));
+    const float mean = s / (float)cols + a.eps;
+    if (mean >= 1e-30f && s < INFINITY) {
+      scale = amax / (127.f * sqrtf(mean));
     } else {
-      // squares past the largest float: the sum of the squares of h / max |h| instead
+      // squares past the largest float, or so small that those which underflow would count (above
+      // 1e-30 they are less than 2^-26 of the mean): the sum of the squares of h / max |h| instead
       float hs = 0.f;
       uint32_t ht = 0;
 #pragma unroll
@@ -190,7 +192,9 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, ctas_per_sm(NORM, TPR))
         }
       ht = 0;
       row_reduce<TPR>(hs, ht, xs, xm);
-      scale = amax / hm / (127.f * sqrtf(hs / (float)cols + a.eps / hm / hm));   // NaN where a value is not finite
+      // (NaN where a value is not finite; eps so far above the squares that its share leaves the range: eps alone)
+      const float e = a.eps / hm / hm;
+      scale = e < INFINITY ? amax / hm / (127.f * sqrtf(hs / (float)cols + e)) : amax / (127.f * sqrtf(a.eps));
     }
   }
   if (t == 0) a.scale[row] = !finite ? __uint_as_float(0x7fc00000u) : top == 0 ? 0.f : scale;
