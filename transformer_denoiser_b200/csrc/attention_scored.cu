@@ -1479,8 +1479,10 @@ __global__ void __launch_bounds__(NT, 2) scored_f32_kernel(const __grid_constant
 // bits, as fp32 has.  Of the nine products of two such sums the six down to 2^-16 are formed
 // (those left out are below 2^-24 of the largest) and added in fp32, smallest first.  Six
 // MMAs at over 16 times the FMA units' rate: 16 heads x 1000 tokens 65 us against 262 in register
-// tiles on the FMA units, 32 x 8 heads x 151 tokens 81 against 137 (two CTAs a head, the
-// second with 23 rows: set-up and latencies).
+// tiles on the FMA units, 32 x 8 heads x 151 tokens 84 against 137 (two CTAs a head, the
+// second with 23 rows: set-up and latencies).  A warp whose rows see none of its keys, or which has
+// no rows, skips the scores (that call 88 -> 84 us; the bf16 kernel, short of registers, got
+// slower by it: 16 heads x 4096 causal 78 -> 88 us).
 // One 128-row tile a CTA, key tiles of 64.  Roles (544 threads): warps 0-7 softmax and output
 // (two threads a row, 32 keys each), warps 8-11 and 12-15 load keys and values, split them and
 // write them as the MMAs read them (128-byte swizzle), warp 16 MMA.  TMEM: two score buffers
@@ -1712,6 +1714,9 @@ scored_split3_kernel(const __grid_constant__ ScoredAttention a, const __grid_con
     const int last = row_ok ? last_key(a, seq, (long)seq.start + i_own) : -1;
     const bool docs = a.q_doc != nullptr;
     int qdoc = docs && row_ok ? a.q_doc[(long)b * a.Sq + i_own] : 0;
+    // documents of this warp's rows: from docs_lo to docs_hi (lo > hi: none)
+    const int docs_lo = __reduce_min_sync(0xffffffffu, row_ok && qdoc >= 0 ? qdoc : INT_MAX);
+    const int docs_hi = __reduce_max_sync(0xffffffffu, row_ok ? qdoc : -1);
     qdoc = qdoc < 0 ? -2 : qdoc;   // a key in no document is staged as -1
     const float slope2 = a.slopes && row_ok ? a.slopes[hk * a.G + g_own] * LOG2E : 0.f;
     int* dbuf = docs_smem + warp * 32;
@@ -1719,9 +1724,15 @@ scored_split3_kernel(const __grid_constant__ ScoredAttention a, const __grid_con
     bool ok = true;
     for (int n = 0; n < n_tiles; ++n) {
       const int j0 = (jt0 + n) * S3_KEYS + half * KH;
+      // no row of this warp sees any of its keys (or it has no rows): their weights are 0 and
+      // nothing is computed
+      bool none = __all_sync(0xffffffffu, j0 > last);
       if (docs) {
         __syncwarp();   // the documents before have been read
-        dbuf[lane] = max(a.kv_doc[(long)b * a.Sk + min(j0 + lane, a.Sk - 1)], -1);
+        const int d = max(a.kv_doc[(long)b * a.Sk + min(j0 + lane, a.Sk - 1)], -1);
+        dbuf[lane] = d;
+        const int lo = __reduce_min_sync(0xffffffffu, d < 0 ? INT_MAX : d), hi = __reduce_max_sync(0xffffffffu, d);
+        none = none || lo > docs_hi || hi < docs_lo;
         __syncwarp();
       }
       // (after a wait that ran out the rest is gone through without waiting, so that the
@@ -1729,33 +1740,37 @@ scored_split3_kernel(const __grid_constant__ ScoredAttention a, const __grid_con
       if (ok) ok = ptx::mbar_wait_bounded(s_bar(n & 1), (n >> 1) & 1, abort, WAIT_LIMIT_NS);
       ptx::tc_fence_after();
       float x[KH];
-      ptx::tmem_ld32(tmem_base + lane_addr + (n & 1) * S3_KEYS + half * KH, x);
-      ptx::tmem_ld_wait();
-      if (a.cap > 0.f) {
+      float top = -INFINITY;
+      if (!none) {
+        ptx::tmem_ld32(tmem_base + lane_addr + (n & 1) * S3_KEYS + half * KH, x);
+        ptx::tmem_ld_wait();
+        if (a.cap > 0.f) {
 #pragma unroll
-        for (int e = 0; e < KH; ++e) x[e] = a.cap * tanhf(x[e] * a.scale / a.cap) * LOG2E;
-      } else {
+          for (int e = 0; e < KH; ++e) x[e] = a.cap * tanhf(x[e] * a.scale / a.cap) * LOG2E;
+        } else {
 #pragma unroll
-        for (int e = 0; e < KH; ++e) x[e] = x[e] * a.scale * LOG2E;
-      }
-      if (a.slopes) {
+          for (int e = 0; e < KH; ++e) x[e] = x[e] * a.scale * LOG2E;
+        }
+        if (a.slopes) {
 #pragma unroll
-        for (int e = 0; e < KH; ++e) x[e] = fmaf(-slope2, fabsf((float)(p - j0 - e)), x[e]);
-      }
-      if (!__all_sync(0xffffffffu, j0 + KH - 1 <= last)) {
+          for (int e = 0; e < KH; ++e) x[e] = fmaf(-slope2, fabsf((float)(p - j0 - e)), x[e]);
+        }
+        if (!__all_sync(0xffffffffu, j0 + KH - 1 <= last)) {
 #pragma unroll
-        for (int e = 0; e < KH; ++e)
-          if (j0 + e > last) x[e] = -INFINITY;
-      }
-      if (docs) {
+          for (int e = 0; e < KH; ++e)
+            if (j0 + e > last) x[e] = -INFINITY;
+        }
+        if (docs) {
 #pragma unroll
-        for (int e = 0; e < KH; ++e)
-          if (dbuf[e] != qdoc) x[e] = -INFINITY;
+          for (int e = 0; e < KH; ++e)
+            if (dbuf[e] != qdoc) x[e] = -INFINITY;
+        }
+        top = max_of(x);
       }
       float* xm = xch + (n & 1) * 2 * TILE;
-      xm[half * TILE + lrow] = max_of(x);
+      xm[half * TILE + lrow] = top;
       pair_sync();
-      const float top = max3(xm[lrow], xm[TILE + lrow], m);
+      top = max3(xm[lrow], xm[TILE + lrow], m);
       const bool move = n == 0 || !(top <= m + RESCALE_AT);
       const float m_new = move ? top : m;
       if (n > 0) {
@@ -1778,21 +1793,27 @@ scored_split3_kernel(const __grid_constant__ ScoredAttention a, const __grid_con
       }
       m = m_new;
       const float ref = m == -INFINITY ? 0.f : m;
+      if (none) {
+        const uint32_t w[16] = {};
 #pragma unroll
-      for (int e = 0; e < KH; ++e) {
-        x[e] = exp2f(x[e] - ref);
-        l += x[e];
-      }
+        for (int t = 0; t < 3; ++t) ptx::tmem_st16(tmem_base + lane_addr + P_COL + t * 32 + half * 16, w);
+      } else {
 #pragma unroll
-      for (int t = 0; t < 3; ++t) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          w[e] = bf16x2_bits(x[2 * e], x[2 * e + 1]);
-          x[2 * e] -= __uint_as_float(w[e] << 16);
-          x[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+        for (int e = 0; e < KH; ++e) {
+          x[e] = exp2f(x[e] - ref);
+          l += x[e];
         }
-        ptx::tmem_st16(tmem_base + lane_addr + P_COL + t * 32 + half * 16, w);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            w[e] = bf16x2_bits(x[2 * e], x[2 * e + 1]);
+            x[2 * e] -= __uint_as_float(w[e] << 16);
+            x[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+          }
+          ptx::tmem_st16(tmem_base + lane_addr + P_COL + t * 32 + half * 16, w);
+        }
       }
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
