@@ -101,6 +101,23 @@ def test_documents_in_any_order():
     _run(9, (2, 3, 333, 4, 2, 128), BF16, q_documents=qd, kv_documents=d)
 
 
+@pytest.mark.parametrize("shape", [(3, 1300, 1300, 2, 1, 64), (1, 40, 5003, 2, 2, 128), (2, 2401, 2401, 8, 8, 64),
+                                   (1, 17, 1024, 1, 1, 64), (2, 300, 897, 2, 2, 128)])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_documents_over_many_key_tiles(shape, cap):
+    """From 8 key tiles on a kernel of its own summarises their documents: odd batches, tokens in no
+    document, numbers up to the largest, lengths that end inside a tile, split keys, two row tiles."""
+    B, Sq, Sk = shape[:3]
+    g = torch.Generator().manual_seed(sum(shape))
+    d = torch.repeat_interleave(torch.arange(Sk), torch.randint(1, 400, (Sk,), generator=g))[:B * Sk].reshape(B, Sk)
+    d = (d - d[:, :1]).to(torch.int32)
+    d[:, 100:131] = -7
+    d[:, Sk - 200:Sk - 150] = 2 ** 31 - 1
+    qd = d[:, Sk - Sq:].contiguous()
+    lengths = torch.tensor([Sk - 37 * b for b in range(B)], dtype=torch.int32)
+    _run(sum(shape), shape, BF16, q_documents=qd.cuda(), kv_documents=d.cuda(), cap=cap, kv_lengths=lengths.cuda())
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("Sq,Sk", [(40, 300), (1, 300), (300, 300)])
 def test_rows_that_see_nothing(Sq, Sk, dtype):

@@ -188,6 +188,9 @@ struct ScoredPlan {
   ScoredConst k;
   float* part_o = nullptr;
   float* part_lse = nullptr;
+  int2* doc_tiles = nullptr;   // [B][key_tiles], documents of the key tiles (null: each CTA looks at the keys)
+  int key_tiles = 0;
+  size_t doc_offset = 0, doc_bytes = 0;   // of doc_tiles in the workspace
   size_t bytes = 0;
 };
 ScoredPlan scored_attention_plan(const ScoredAttention& a, bool is_bf16, int num_sms);
