@@ -101,7 +101,7 @@ def test_documents_in_any_order():
     _run(9, (2, 3, 333, 4, 2, 128), BF16, q_documents=qd, kv_documents=d)
 
 
-@pytest.mark.parametrize("shape", [(3, 1300, 1300, 2, 1, 64), (1, 40, 5003, 2, 2, 128), (2, 2401, 2401, 8, 8, 64),
+@pytest.mark.parametrize("shape", [(3, 1300, 1300, 2, 1, 64), (1, 40, 5003, 2, 2, 128), (5, 1025, 1025, 8, 8, 64),
                                    (1, 17, 1024, 1, 1, 64), (2, 300, 897, 2, 2, 128)])
 @pytest.mark.parametrize("cap", [0.0, 30.0])
 def test_documents_over_many_key_tiles(shape, cap):
@@ -116,6 +116,31 @@ def test_documents_over_many_key_tiles(shape, cap):
     qd = d[:, Sk - Sq:].contiguous()
     lengths = torch.tensor([Sk - 37 * b for b in range(B)], dtype=torch.int32)
     _run(sum(shape), shape, BF16, q_documents=qd.cuda(), kv_documents=d.cuda(), cap=cap, kv_lengths=lengths.cuda())
+
+
+@pytest.mark.parametrize("shape", [(9, 75, 140, 16, 8, 64), (20, 129, 33, 4, 4, 128)])
+@pytest.mark.parametrize("options", ["lengths", "documents", "all", "poison"])
+def test_fp32_rows_left_behind_whole_tiles(shape, options):
+    """Heads whose last CTA has few rows (22 that share tokens with the one before, 1): warps without rows."""
+    B, Sq, Sk, Hq = shape[:4]
+    g = torch.Generator().manual_seed(Sq)
+    lengths = torch.randint(0, Sk + 1, (B,), generator=g, dtype=torch.int32)
+    if options == "poison":
+        q, k, v = _qkv(Sk, *shape, FP32)
+        for b in range(B):
+            k[b, lengths[b]:] = float("nan")
+            v[b, lengths[b]:] = float("inf")
+        check_attention(kb.attention_scored(q, k, v, kv_lengths=lengths.cuda()), q, k, v, kv_lengths=lengths.cuda())
+        return
+    kw = {}
+    if options != "documents":
+        kw |= dict(kv_lengths=lengths.cuda(), slopes=(torch.arange(Hq) / 37).cuda())
+    if options != "lengths":
+        d = torch.randint(-1, 3, (B, max(Sq, Sk)), generator=g, dtype=torch.int32).cuda()
+        kw |= dict(q_documents=d[:, :Sq].contiguous(), kv_documents=d[:, :Sk].contiguous())
+    if options == "all":
+        kw |= dict(causal=True, cap=20.0, prefix=torch.randint(0, 9, (B,), generator=g, dtype=torch.int32).cuda())
+    _run(Sq, shape, FP32, **kw)
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
