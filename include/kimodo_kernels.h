@@ -183,7 +183,7 @@ KIMODO_API int kimodo_gemm_int8(const void* A, long long lda, const float* a_sca
  *   Positions must stay within +-2^30.
  * 1 <= batch, q_len; 0 <= kv_len; q_len, kv_len <= KIMODO_MAX_KEYS.
  * workspace: device memory of at least the bytes that kimodo_attention_scored_workspace
- *   gives for the same sizes (0 for most), 16-byte aligned, the caller's until the call's
+ *   gives for the same arguments (0 for many), 16-byte aligned, the caller's until the call's
  *   work is done; calls that may overlap (streams, captured graphs) need their own.
  */
 #define KIMODO_MAX_KEYS 16777216
