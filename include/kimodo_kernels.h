@@ -160,7 +160,7 @@ KIMODO_API int kimodo_gemm_int8(const void* A, long long lda, const float* a_sca
  * kimodo_attention_* with other head layouts, lengths, score forms and masks.  Query i of
  * sequence b has position p_i = q_start[b] + i; for query head h and key j:
  *   x_ij = scale q_i . k_j
- *   x_ij = cap tanh(x_ij / cap)          if cap > 0
+ *   x_ij = cap tanh(x_ij / cap)          if cap > 0 (any finite cap of at least |scale| / 1e6)
  *   x_ij = x_ij - slopes[h] |p_i - j|    if slopes
  * Key j is seen if j < kv_lengths[b], and, with causal, j <= p_i or j < prefix[b], and, with
  * documents, q_documents[b, i] == kv_documents[b, j] >= 0 (a negative number: in no

@@ -65,32 +65,44 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // cap * tanh(x / cap) in log2 units, x = scale s.  For |x| <= cap / 2: s times a polynomial of degree
-// 3 in s^2 for tanh(z) / z (weighted least squares towards the relative minimax on
+// 3 in z^2, z = x / cap, for tanh(z) / z (weighted least squares towards the relative minimax on
 // [0, 1/4] in z^2; relative error 5.5e-7, on a cap of 50 at most 2e-5 of a weight, a
 // hundredth of its rounding to bf16).  It costs no special-function slots, which bound
-// the softmax.  Beyond, tanh z = 1 - 2 / (1 + e^(2z)).
+// the softmax.  Beyond, tanh z = 1 - 2 / (1 + e^(2z)), whose error is that of the cap: a small
+// score never takes that form, whatever the other scores of the warp are.
+__host__ __device__ constexpr float cap_poly(int i) {
+  return i == 0 ? 0.999999463558197f : i == 1 ? -0.33326318860054016f : i == 2 ? 0.13190296292304993f : -0.044402219355106354f;
+}
 ScoredConst scored_const(float scale, float cap) {
   const float sc = scale == 0.f ? 1.f : fabsf(scale), lin = sc * LOG2E, z = cap > 0.f ? sc / cap : 0.f;
-  const float r[4] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.044402219355106354f};
   ScoredConst k;
   k.lin = make_float2(lin, lin);
   float f = lin;
   for (int i = 0; i < 4; ++i) {
-    k.c[i] = make_float2(r[i] * f, r[i] * f);
+    k.c[i] = make_float2(cap_poly(i) * f, cap_poly(i) * f);
     f *= z * z;
   }
-  // (below 1e-5 the powers of z would leave the floats' range)
-  k.limit2 = z > 1e-5f ? 0.25f / (z * z) : 0.f;
+  // Below 1e-5 the higher coefficients may underflow; they are not needed while x is below a
+  // 64th of the cap (the terms of degree 4 and 6 in z are then below 1e-8).
+  const double z2 = (double)z * z;
+  k.limit2 = z > 1e-5f ? (float)(0.25 / z2) : z2 > 2.5e-34 ? (float)(2.4e-4 / z2) : 1e30f;
+  // scales and caps that take a coefficient out of the floats' range leave every score to capped_any
+  if (lin < 1e-6f || !isfinite(k.c[3].x)) k.limit2 = -1.f;
+  k.z = z;
   k.two = 2.f * LOG2E * z;
   k.cap2 = cap * LOG2E;
   return k;
 }
-// two scores at once (f32x2 arithmetic); t = s^2
+// two scores at once (f32x2 arithmetic); t = s^2 up to limit2
 __device__ __forceinline__ float2 cap_ratio(const ScoredConst& k, float2 t) {
   return __ffma2_rn(__ffma2_rn(__ffma2_rn(k.c[3], t, k.c[2]), t, k.c[1]), t, k.c[0]);
 }
+// any score
 __device__ __forceinline__ float capped_any(const ScoredConst& k, float s) {
-  return fmaf(-2.f * k.cap2, rcp_approx(1.f + ex2(s * k.two)), k.cap2);
+  const float zs = s * k.z, t = zs * zs;
+  const float ratio = fmaf(fmaf(fmaf(cap_poly(3), t, cap_poly(2)), t, cap_poly(1)), t, cap_poly(0));
+  const float far = fmaf(-2.f * k.cap2, rcp_approx(1.f + ex2(s * k.two)), k.cap2);
+  return t <= 0.25f ? s * k.lin.x * ratio : far;
 }
 template <int N>
 __device__ __forceinline__ void cap_scores(const ScoredConst& k, float (&x)[N]) {

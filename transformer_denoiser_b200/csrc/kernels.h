@@ -177,6 +177,7 @@ struct ScoredConst {
   float2 lin;            // |scale| * log2 e (a scale of 0 counts as 1: its scores are made 0)
   float2 c[4];           // tanh(z) / z * lin as a polynomial in s^2, z = |scale| s / cap
   float limit2;          // s^2 up to which it holds
+  float z;               // |scale| / cap
   float two, cap2;       // e^(2 z) = 2^(two s); cap * log2 e
 };
 // Split of a call over CTAs and keys; parts > 1: results of each part and their weights in a
