@@ -180,7 +180,10 @@ KIMODO_API int kimodo_gemm_int8(const void* A, long long lda, const float* a_sca
  *   q_documents int32 [batch, q_len], kv_documents int32 [batch, kv_len] (both or
  *   neither).  NULL switches an option off; kv_lengths NULL: kv_len (lengths are clamped to
  *   [0, kv_len]); q_start NULL: kv_len - q_len (the queries are the last tokens).
- *   Positions must stay within +-2^30.
+ *   A row's distances are counted from the nearest position that its length and causal masks let
+ *   it see (the softmax cancels the constant), so a query far from all its keys, on either
+ *   side, keeps their differences.  A bias is right to |slope| d 2^-20, d that distance: with
+ *   documents, to the distance at which the row's own document lies.
  * 1 <= batch, q_len; 0 <= kv_len; q_len, kv_len <= KIMODO_MAX_KEYS.
  * workspace: device memory of at least the bytes that kimodo_attention_scored_workspace
  *   gives for the same arguments (0 for many), 16-byte aligned, the caller's until the call's

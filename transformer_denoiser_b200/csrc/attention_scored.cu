@@ -172,6 +172,13 @@ __device__ __forceinline__ int last_key(const ScoredAttention& a, const SeqInfo&
   }
   return j;
 }
+// Position that a row's distances are counted from: the nearest one that length, position and prefix
+// let it see.  It differs from p by a constant of the row for all its keys, which the softmax
+// cancels; counted from p itself, slope * distance would round the differences between keys
+// away where all of them are far (a slope of 0.5 at a distance of 10^6: 3 % of a weight).
+__device__ __forceinline__ int bias_position(long p, int last) {
+  return p > last ? max(last, 0) : p < 0 ? 0 : (int)p;
+}
 
 // ---------------------------------------------------------------- one row by one warp, fp32
 // The definition, over the seen keys alone: scores by warp-shuffle dot products, online
@@ -183,7 +190,7 @@ __device__ __noinline__ void row_by_warp(const ScoredAttention& a, int b, int hq
   const int hk = hq / a.G;
   const SeqInfo s = sequence_info(a, b);
   const long p = (long)s.start + i;
-  const int last = last_key(a, s, p);
+  const int last = last_key(a, s, p), from = bias_position(p, last);
   const T* q = static_cast<const T*>(a.q) + b * a.q_batch + i * a.q_token + hq * a.q_head + lane * PER;
   const T* k = static_cast<const T*>(a.k) + b * a.k_batch + hk * a.k_head + lane * PER;
   const T* v = static_cast<const T*>(a.v) + b * a.v_batch + hk * a.v_head + lane * PER;
@@ -205,10 +212,7 @@ __device__ __noinline__ void row_by_warp(const ScoredAttention& a, int b, int hq
     for (int off = 16; off; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
     float x = d * a.scale;
     if (a.cap > 0.f) x = a.cap * tanhf(x / a.cap);
-    if (a.slopes) {
-      const long dist = p - j;
-      x -= slope * (float)(dist < 0 ? -dist : dist);
-    }
+    if (a.slopes) x -= slope * fabsf((float)(from - j));
     if (x == -INFINITY) continue;   // weight 0, whatever the value is
     const float mn = fmaxf(m, x);
     const float f = expf(m - mn), w = expf(x - mn);
@@ -659,8 +663,8 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const int pair_bar = 1 + t * 4 + (warp & 3);       // the two warps that share 32 rows
     auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
     const bool warp_rows = (warp & 3) * 32 + row0 + t * TILE < rows;
-    const int p = seq.start + i_own;
     const int last = row_ok ? last_key(a, seq, (long)seq.start + i_own) : -1;
+    const int p = bias_position((long)seq.start + i_own, last);
     qdoc = qdoc < 0 ? -2 : qdoc;
     const float slope2 = BIAS && row_ok ? a.slopes[hk * a.G + g_own] * LOG2E : 0.f;
     // the constants are those of |scale|: the products take its sign, and a scale of 0 is products of 0
@@ -1016,7 +1020,7 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       const bool ok = r < rows;
       const int i = ok ? r / a.G : 0, g = ok ? r - i * a.G : 0;
       row_last[r] = ok ? last_key(a, seq, (long)seq.start + i) : -1;
-      row_pos[r] = seq.start + i;
+      row_pos[r] = bias_position((long)seq.start + i, row_last[r]);
       row_doc[r] = ok && a.q_doc ? a.q_doc[(long)b * a.Sq + i] : 0;
       row_slope[r] = ok && a.slopes ? a.slopes[hk * a.G + g] * LOG2E : 0.f;
       bad[r] = 0;
@@ -1384,8 +1388,8 @@ __global__ void __launch_bounds__(NT, 2) scored_f32_kernel(const __grid_constant
     const int r = row0 + rg + RG * u;
     const bool ok = r < rows;
     const int i = ok ? r / a.G : 0, g = ok ? r - i * a.G : 0;
-    pos[u] = seq.start + i;
     last[u] = ok ? last_key(a, seq, (long)seq.start + i) : -1;
+    pos[u] = bias_position((long)seq.start + i, last[u]);
     doc[u] = ok && a.q_doc ? a.q_doc[(long)b * a.Sq + i] : 0;
     slope[u] = ok && a.slopes ? a.slopes[hk * a.G + g] * LOG2E : 0.f;
     m[u] = -INFINITY;
@@ -1761,8 +1765,8 @@ scored_split3_kernel(const __grid_constant__ ScoredAttention a, const __grid_con
     const int r_own = row0 + lrow;
     const bool row_ok = r_own < rows;
     const int i_own = row_ok ? r_own / a.G : 0, g_own = row_ok ? r_own - i_own * a.G : 0;
-    const int p = seq.start + i_own;
     const int last = row_ok ? last_key(a, seq, (long)seq.start + i_own) : -1;
+    const int p = bias_position((long)seq.start + i_own, last);
     const bool docs = a.q_doc != nullptr;
     int qdoc = docs && row_ok ? a.q_doc[(long)b * a.Sq + i_own] : 0;
     // documents of this warp's rows: from docs_lo to docs_hi (lo > hi: none)
