@@ -31,9 +31,10 @@
 // polynomial's range) shows that this was wrong, and in masked tiles, the maximum is taken,
 // the reference moved and O rescaled.
 //
-// Masked places never reach a result: a masked score is replaced, value rows past kv_len are
-// zeroed in shared memory, and a row whose result is not finite (a NaN or infinity among
-// values with weight 0 in its tile) is computed again over the seen keys alone.
+// Masked places never reach a result: a masked score is replaced, value rows past the last key
+// that a CTA's rows see are zeroed in shared memory (a cache may hold anything behind its
+// newest token), and a row whose result is still not finite (a NaN or infinity among values
+// with weight 0 in its tile) is computed again over the seen keys alone, slowly.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -263,7 +264,7 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
 struct RowTile {
   int docs_lo, docs_hi;   // smallest and largest document of its rows (lo > hi: none)
   int any_none;           // a row in no document
-  int pad;
+  int key_end;            // of tile 0: the keys that the CTA's rows see end here
 };
 
 // Summary of a key tile's documents, its keys spread over a warp (-1: no document): x = the
@@ -410,6 +411,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   // ---------------- key tiles of this CTA
   const int row_last = min(row0 + TILES * TILE, rows) - 1;
   const int key_end = 1 + last_key(a, seq, (long)seq.start + row_last / a.G);
+  if (threadIdx.x == 0) tiles[0].key_end = key_end;
   const int jt_all = (key_end + TILE - 1) / TILE;
   const int jt0 = min(split * plan.tiles_per_split, jt_all);
   const int jt1 = plan.splits == 1 ? jt_all : min(jt0 + plan.tiles_per_split, jt_all);
@@ -544,7 +546,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       };
       auto p_ready = [&]() {   // the pending key tile's values and weights
         if (!wait(full_bar(v_stage), v_phase)) return;
-        if (v_rows < TILE) {   // value rows past the last key: 0, whatever they hold
+        if (v_rows < TILE) {   // value rows past the last key that a row of this CTA sees: 0, whatever they hold
           uint8_t* v = smem + TILES * C::Q_BYTES + v_stage * C::KV_BYTES;
           const int n = (TILE - v_rows) * 8;
           for (int c = lane; c < n * (HD / 64); c += 32) {
@@ -619,7 +621,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             pend = true;
             v_stage = stage;
             v_phase = phase;
-            v_rows = min(seq.kv_len - jt * TILE, TILE);
+            v_rows = min(tiles[0].key_end - jt * TILE, TILE);   // (shared memory: registers are short)
           }
           unlock();
         }
@@ -1093,8 +1095,8 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       const int vs = stage_of(2 * n + 1);
       if (ok) ok = ptx::mbar_wait_bounded(full_bar(vs), phase_of(2 * n + 1), abort, WAIT_LIMIT_NS);
       if (!ok) break;
-      const int v_rows = min(seq.kv_len - (jt0 + n) * TILE, TILE);
-      if (v_rows < TILE) {   // value rows past the last key: 0, whatever they hold
+      const int v_rows = min(key_end - (jt0 + n) * TILE, TILE);
+      if (v_rows < TILE) {   // value rows past the last key that a row of this CTA sees: 0, whatever they hold
         uint8_t* v = smem + C::Q_BYTES + C::P_BYTES + (size_t)vs * C::KV_BYTES;
         const int cnt = (TILE - v_rows) * 8;
         for (int c = lane; c < cnt * (HD / 64); c += 32) {
@@ -1354,13 +1356,13 @@ __global__ void __launch_bounds__(NT, 2) scored_f32_kernel(const __grid_constant
   const bool docs = a.q_doc != nullptr;
   const float* kb = static_cast<const float*>(a.k) + b * a.k_batch + hk * a.k_head;
   const float* vb = static_cast<const float*>(a.v) + b * a.v_batch + hk * a.v_head;
-  // one tile's rows into shared memory, those past the last key as zeros
+  // one tile's rows into shared memory, those past the last key that a row sees as zeros
   auto fetch = [&](float* dst, const float* src, long stride, int j0) {
     const uint32_t d0 = ptx::smem_u32(dst);
 #pragma unroll 4
     for (int c = threadIdx.x; c < FT * (HD / 4); c += NT) {
       const int lj = c / (HD / 4), ch = c % (HD / 4), j = j0 + lj;
-      const bool in = j < seq.kv_len;
+      const bool in = j < key_end;
       ptx::cp_async_16_zfill(d0 + (uint32_t)(lj * LD + ch * 4) * 4, src + (in ? j : 0) * stride + ch * 4, in);
     }
     ptx::cp_async_commit();
@@ -1652,7 +1654,7 @@ scored_split3_kernel(const __grid_constant__ ScoredAttention a, const __grid_con
       for (int u = 0; u < TASKS; ++u) {
         const int task = l + 128 * u, j = j0 + task / CH;
         lo[u] = hi[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < seq.kv_len) {
+        if (j < key_end) {   // the last key that a row of this CTA sees; zeros behind it
           const float* p = src + j * stride + (task % CH) * 8;
           lo[u] = *reinterpret_cast<const float4*>(p);
           hi[u] = *reinterpret_cast<const float4*>(p + 4);
