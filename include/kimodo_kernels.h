@@ -142,7 +142,7 @@ KIMODO_API int kimodo_rms_norm_int8(const void* x, long long ldx, int x_bf16, co
  * The sum is exact (32-bit integers): results do not depend on how the work is split.
  * A: int8 [M, K], row stride lda; W: int8 [N, K], row stride ldw; both 16-byte aligned with
  * lda, ldw multiples of 16 (columns past K are not read into the sum).  1 <= K <=
- * KIMODO_INT8_MAX_K, the largest K whose sum cannot leave 32 bits.
+ * KIMODO_INT8_MAX_K, the largest K whose sum cannot leave 32 bits; M, N <= KIMODO_INT8_MAX_ROWS.
  * a_scale: fp32 [M]; w_scale: fp32 [N]; bias: fp32 [N] or NULL.
  * epilogue: KIMODO_EPI_*; resid fp32 [M, ldr] with KIMODO_EPI_BIAS_RESID (may equal out),
  * ignored otherwise.  out: bf16 (out_f32 = 0) or fp32 (1), row stride ldo, no alignment
@@ -150,6 +150,7 @@ KIMODO_API int kimodo_rms_norm_int8(const void* x, long long ldx, int x_bf16, co
  * overlap A or W, nor resid unless it equals it (in place, same stride).
  */
 #define KIMODO_INT8_MAX_K 131071
+#define KIMODO_INT8_MAX_ROWS 2147483135 /* 2^31 - 513 */
 KIMODO_API int kimodo_gemm_int8(const void* A, long long lda, const float* a_scale, const void* W, long long ldw,
                                 const float* w_scale, const float* bias, const float* resid, long long ldr,
                                 void* out, long long ldo, int M, int N, int K, int epilogue, int out_f32,

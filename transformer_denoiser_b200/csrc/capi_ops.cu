@@ -130,6 +130,9 @@ int kimodo_gemm_int8(const void* A, long long lda, const float* a_scale, const v
   clear_error();
   if (!A || !a_scale || !W || !w_scale || !out) return set_error(KIMODO_EINVAL, "NULL tensor argument");
   if (M < 1 || N < 1 || K < 1) return set_error(KIMODO_EINVAL, "M, N, K must be >= 1");
+  // the kernels go past the last row by up to two tiles in 32-bit integers
+  if (M > KIMODO_INT8_MAX_ROWS || N > KIMODO_INT8_MAX_ROWS)
+    return set_error(KIMODO_EINVAL, "M and N must be at most %d (got %d, %d)", KIMODO_INT8_MAX_ROWS, M, N);
   if (K > KIMODO_INT8_MAX_K)
     return set_error(KIMODO_EINVAL, "K must be at most %d (32-bit sums; got %d)", KIMODO_INT8_MAX_K, K);
   if (lda < K || ldw < K || ldo < N) return set_error(KIMODO_EINVAL, "leading dimensions must cover K / N");

@@ -520,7 +520,7 @@ cudaError_t launch_pair(const GemmI8& g, const I8Epi& ep, DevError* err, cudaStr
     return cudaErrorInvalidValue;
   const int nw = (g.N + 255) / 256, nt = (g.M + BN - 1) / BN;
   const long tiles = (long)nw * nt;
-  if (tiles > INT_MAX) return cudaErrorInvalidValue;
+  if (tiles > INT_MAX - num_sms) return cudaErrorInvalidValue;   // (a CTA steps past the last tile by the grid)
   const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
