@@ -23,3 +23,17 @@ def test_products_of_nearly_2_31_rows(lib, M, N, epi):
     rc = lib.kimodo_gemm_int8(P, 16, P, 2 * P, 16, P, None, P, N, 3 * P, N, M, N, 16, epi, 1 if epi == 3 else 0, None)
     assert rc == -1, rc
     assert b"at most 2147483135" in lib.kimodo_last_error()
+
+
+@pytest.mark.parametrize("batch,q_len,heads", [(2 ** 30, 2 ** 24, 2 ** 10), (2 ** 30, 2 ** 20, 2 ** 14), (2 ** 24, 2 ** 24, 2 ** 17),
+                                               (2 ** 31 - 1, 2 ** 24, 2 ** 30)])
+def test_query_rows_whose_number_leaves_64_bits(lib, batch, q_len, heads):
+    """Their product wraps to zero or below."""
+    s = (ctypes.c_longlong * 3)(2 ** 35, 64, 64)
+    a = kb.ScoredAttention(P, P, P, 2 * P, None, None, None, None, None, None, s, s, s, s, batch, q_len, 8, heads, heads,
+                           64, kb.BF16, 0, 0.125, 0.0)
+    n = ctypes.c_size_t(77)
+    for rc in (lib.kimodo_attention_scored(ctypes.byref(a), None, 0, None),
+               lib.kimodo_attention_scored_workspace(ctypes.byref(a), ctypes.byref(n))):
+        assert rc == -1, rc
+        assert b"too many query rows" in lib.kimodo_last_error()

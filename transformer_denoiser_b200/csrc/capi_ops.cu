@@ -180,7 +180,8 @@ int scored_args(const kimodo_scored_attention* p, ScoredAttention* a) {
     return set_error(KIMODO_EINVAL, "dtype must be KIMODO_FP32 or KIMODO_BF16 (got %d)", p->dtype);
   if (p->kv_len > KIMODO_MAX_KEYS || p->q_len > KIMODO_MAX_KEYS)
     return set_error(KIMODO_EINVAL, "q_len and kv_len must be at most %d", KIMODO_MAX_KEYS);
-  if ((long long)p->batch * p->q_len * p->q_heads > INT_MAX / 2)
+  // (two steps: the product of all three can leave 64 bits)
+  if ((long long)p->batch * p->q_len > INT_MAX / 2 || (long long)p->batch * p->q_len * p->q_heads > INT_MAX / 2)
     return set_error(KIMODO_EINVAL, "too many query rows");
   if (!isfinite(p->scale)) return set_error(KIMODO_EINVAL, "scale must be finite");
   if (!isfinite(p->cap) || p->cap < 0.f) return set_error(KIMODO_EINVAL, "cap must be finite and >= 0");
