@@ -70,11 +70,53 @@ int check_type(const char* what, const void* p, int bf16_flag) {
   return KIMODO_OK;
 }
 
-// An output that starts where an input does: rows would be overwritten that other threads, or
-// the same call again (attention's rows with non-finite results), still read.
-int check_apart(const char* what, const void* out, std::initializer_list<const void*> inputs) {
-  for (const void* p : inputs)
-    if (p != nullptr && p == out) return set_error(KIMODO_EINVAL, "%s must not overlap the inputs", what);
+// Where a tensor lies: `width` consecutive bytes, repeated along up to three dimensions.
+struct Place {
+  const void* p;
+  long long width;
+  long long extent[3] = {1, 1, 1};
+  long long stride[3] = {0, 0, 0};   // bytes, >= 0
+};
+Place place_of_rows(const void* p, long long rows, long long cols, long long ld, int elem) {
+  return Place{p, cols * elem, {rows, 1, 1}, {ld * elem, 0, 0}};
+}
+
+using Wide = __int128;   // extents times strides can leave 64 bits
+
+// Whether two tensors have no byte in common.  Where their ranges meet, they may still be parts of one
+// buffer (columns of the same rows, heads of the same tokens): modulo a stride of either, each
+// then stays in a window, and the windows do not meet.
+bool apart(const Place& a, const Place& b) {
+  const Place* t[2] = {&a, &b};
+  const Wide d = (Wide)reinterpret_cast<uintptr_t>(b.p) - (Wide)reinterpret_cast<uintptr_t>(a.p);
+  Wide span[2];
+  for (int i = 0; i < 2; ++i) {
+    span[i] = t[i]->width;
+    for (int e = 0; e < 3; ++e) span[i] += (Wide)(t[i]->extent[e] - 1) * t[i]->stride[e];
+  }
+  if (d >= span[0] || -d >= span[1]) return true;
+  for (int c = 0; c < 6; ++c) {
+    if (t[c / 3]->extent[c % 3] <= 1) continue;
+    const Wide period = t[c / 3]->stride[c % 3];
+    if (period <= 0) continue;
+    Wide window[2];
+    for (int i = 0; i < 2; ++i) {
+      window[i] = t[i]->width;
+      for (int e = 0; e < 3; ++e)
+        if (t[i]->extent[e] > 1 && t[i]->stride[e] % period != 0)
+          window[i] += (Wide)(t[i]->extent[e] - 1) * t[i]->stride[e];
+    }
+    const Wide at = ((d % period) + period) % period;
+    if (at >= window[0] && at + window[1] <= period) return true;
+  }
+  return false;
+}
+
+// An output that meets an input: rows would be overwritten that other threads, or the same call again
+// (attention's rows with non-finite results), still read.
+int check_apart(const char* what, const Place& out, std::initializer_list<Place> inputs) {
+  for (const Place& in : inputs)
+    if (in.p != nullptr && !apart(out, in)) return set_error(KIMODO_EINVAL, "%s must not overlap the inputs", what);
   return KIMODO_OK;
 }
 
@@ -88,7 +130,7 @@ int kimodo_quantize_int8(const void* x, long long ldx, int x_bf16, void* q, long
   KD_TRY(check_rows(x, ldx, q, ldq, scale, rows, cols));
   KD_TRY(check_type("x", x, x_bf16));
   if (misaligned(scale, 4)) return set_error(KIMODO_EINVAL, "scale is not aligned to its elements");
-  KD_TRY(check_apart("q", q, {x}));
+  KD_TRY(check_apart("q", place_of_rows(q, rows, cols, ldq, 1), {place_of_rows(x, rows, cols, ldx, x_bf16 ? 2 : 4)}));
   KD_TRY(check_here({x, q, scale}));
   RowsInt8 a;
   a.x = x; a.ldx = ldx; a.q = static_cast<int8_t*>(q); a.ldq = ldq; a.scale = scale; a.rows = rows; a.cols = cols;
@@ -114,8 +156,14 @@ int kimodo_rms_norm_int8(const void* x, long long ldx, int x_bf16, const void* r
   }
   if (misaligned(scale, 4) || misaligned(gamma, 4))
     return set_error(KIMODO_EINVAL, "gamma and scale must be aligned to their elements");
-  KD_TRY(check_apart("resid_out", resid_out, {x}));
-  KD_TRY(check_apart("q", q, {x, resid, resid_out}));
+  const Place xs = place_of_rows(x, rows, cols, ldx, x_bf16 ? 2 : 4);
+  const Place rs = place_of_rows(resid, rows, cols, ldr, resid_bf16 ? 2 : 4);
+  const Place ros = place_of_rows(resid_out, rows, cols, ldro, resid_bf16 ? 2 : 4);
+  if (resid) {
+    KD_TRY(check_apart("resid_out", ros, {xs}));
+    if (resid != resid_out) KD_TRY(check_apart("resid_out", ros, {rs}));
+  }
+  KD_TRY(check_apart("q", place_of_rows(q, rows, cols, ldq, 1), {xs, rs, ros}));
   KD_TRY(check_here({x, resid, resid_out, gamma, q, scale}));
   RowsInt8 a;
   a.x = x; a.ldx = ldx; a.r_in = resid; a.ldr_in = ldr; a.r_out = resid_out; a.ldr_out = ldro; a.gamma = gamma;
@@ -150,7 +198,10 @@ int kimodo_gemm_int8(const void* A, long long lda, const float* a_scale, const v
   if (misaligned(out, out_f32 ? 4 : 2) || misaligned(a_scale, 4) || misaligned(w_scale, 4) || misaligned(bias, 4) ||
       misaligned(resid, 4))
     return set_error(KIMODO_EINVAL, "out, resid, bias and scales must be aligned to their elements");
-  KD_TRY(check_apart("out", out, {A, W}));
+  const bool resid_used = epilogue == KIMODO_EPI_BIAS_RESID && resid != out;
+  KD_TRY(check_apart("out", place_of_rows(out, M, N, ldo, out_f32 ? 4 : 2),
+                     {place_of_rows(A, M, K, lda, 1), place_of_rows(W, N, K, ldw, 1),
+                      place_of_rows(resid_used ? resid : nullptr, M, N, ldr, 4)}));
   if (!gemm_tc_available()) return set_error(KIMODO_EUNSUPPORTED, "cuTensorMapEncodeTiled is unavailable");
   KD_TRY(check_here({A, a_scale, W, w_scale, bias, epilogue == KIMODO_EPI_BIAS_RESID ? resid : nullptr, out}));
   const int sms = current_sms();
@@ -249,7 +300,12 @@ int kimodo_attention_scored(const kimodo_scored_attention* args, void* workspace
   clear_error();
   ScoredAttention a;
   KD_TRY(scored_args(args, &a));
-  KD_TRY(check_apart("out", a.out, {a.q, a.k, a.v}));
+  const long long e = args->dtype == KIMODO_BF16 ? 2 : 4, w = a.HD * e;
+  const Place out{a.out, w, {a.B, a.Sq, a.Hq}, {a.o_batch * e, a.o_token * e, a.o_head * e}};
+  const Place q{a.q, w, {a.B, a.Sq, a.Hq}, {a.q_batch * e, a.q_token * e, a.q_head * e}};
+  const Place k{a.Sk > 0 ? a.k : nullptr, w, {a.B, a.Sk, a.Hkv}, {a.k_batch * e, a.k_token * e, a.k_head * e}};
+  const Place v{a.Sk > 0 ? a.v : nullptr, w, {a.B, a.Sk, a.Hkv}, {a.v_batch * e, a.v_token * e, a.v_head * e}};
+  KD_TRY(check_apart("out", out, {q, k, v}));
   KD_TRY(check_here({a.q, a.k, a.v, a.out, a.slopes, a.prefix, a.q_doc, a.kv_doc, a.kv_lengths, a.q_start}));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = args->dtype == KIMODO_BF16;
