@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(128 + 256 * TILES, TILES == 2 ? 1 : 2)   // 96
 scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ ScoredAttention a, const __grid_constant__ ScoredPlan plan,
                  DevError* err) {
+  static_assert(CAP || TILES == 1, "two row tiles are taken under a cap only");
   using C = Cfg<HD, TILES>;
   constexpr int STAGES = C::STAGES, NUM_THREADS = C::THREADS;
   extern __shared__ uint8_t smem_raw[];
@@ -1135,16 +1136,13 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const int quarter = warp & 3, sw = warp - 2, key = quarter * 32 + lane;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
     const uint32_t o_addr = tmem_base + lane_addr + 2 * NR;
-    constexpr int RL = (NR + 31) / 32;          // rows kept per lane
     const bool cap = a.cap > 0.f, bias = a.slopes != nullptr, docs = a.q_doc != nullptr;
     const ScoredConst& cc = plan.k;
     const float sc = a.scale == 0.f ? 0.f : copysignf(cc.lin.x, a.scale);
     const int all_see = row_last[0];            // keys up to here are seen by every row
     float* refs = wref + sw * 2 * NR;
     float* facs = refs + NR;
-    float my_ref[RL], l[NR];
-#pragma unroll
-    for (int c = 0; c < RL; ++c) my_ref[c] = -INFINITY;
+    float my_ref = -INFINITY, l[NR];            // reference of row `lane`
 #pragma unroll
     for (int r = 0; r < NR; ++r) l[r] = 0.f;
     bool ok = true;
@@ -1185,30 +1183,22 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       }
       // row maxima over the tile: within the warp, then over the four
       float* wm = wmax + (n & 1) * 4 * NR;
+      float keep = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < RL; ++c) {
-        float keep = -INFINITY;
-#pragma unroll
-        for (int r = 32 * c; r < 32 * c + 32 && r < NR; ++r) {
-          const float v = warp_max(x[r]);
-          if (lane == (r & 31)) keep = v;
-        }
-        if (32 * c + lane < NR) wm[sw * NR + 32 * c + lane] = keep;
+      for (int r = 0; r < NR; ++r) {
+        const float v = warp_max(x[r]);
+        if (lane == r) keep = v;
       }
+      if (lane < NR) wm[sw * NR + lane] = keep;
       asm volatile("bar.sync 1, 128;" ::: "memory");
       bool any = false;
-#pragma unroll
-      for (int c = 0; c < RL; ++c) {
-        const int r = 32 * c + lane;
-        if (r < NR) {
-          const float top = fmaxf(fmaxf(wm[r], wm[NR + r]), fmaxf(wm[2 * NR + r], wm[3 * NR + r]));
-          const bool move = n == 0 || top > my_ref[c] + RESCALE_AT;
-          const float next = move ? fmaxf(my_ref[c], top) : my_ref[c];
-          facs[r] = next == my_ref[c] ? 1.f : ex2(my_ref[c] - next);
-          any |= move;
-          my_ref[c] = next;
-          refs[r] = next == -INFINITY ? 0.f : next;
-        }
+      if (lane < NR) {
+        const float top = fmaxf(fmaxf(wm[lane], wm[NR + lane]), fmaxf(wm[2 * NR + lane], wm[3 * NR + lane]));
+        any = n == 0 || top > my_ref + RESCALE_AT;
+        const float next = any ? fmaxf(my_ref, top) : my_ref;
+        facs[lane] = next == my_ref ? 1.f : ex2(my_ref - next);
+        my_ref = next;
+        refs[lane] = next == -INFINITY ? 0.f : next;
       }
       any = __any_sync(0xffffffffu, any);   // the same in all four warps
       __syncwarp();
@@ -1216,19 +1206,16 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         if (ok) ok = ptx::mbar_wait_bounded(o_bar, (n - 1) & 1, abort, WAIT_LIMIT_NS);   // P and O of tile n - 1
         if (any) {
           ptx::tc_fence_after();
+          float v[NR];
+          uint32_t w[NR];
+          ptx::tmem_ld(o_addr, v);
+          ptx::tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < NR; c += 16) {
-            float v[16];
-            uint32_t w[16];
-            ptx::tmem_ld(o_addr + c, v);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              w[e] = __float_as_uint(v[e] * facs[c + e]);
-              l[c + e] *= facs[c + e];
-            }
-            ptx::tmem_st16(o_addr + c, w);
+          for (int r = 0; r < NR; ++r) {
+            w[r] = __float_as_uint(v[r] * facs[r]);
+            l[r] *= facs[r];
           }
+          ptx::tmem_st16(o_addr, w);
           ptx::tmem_st_wait();
         }
       }
@@ -1254,7 +1241,7 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       float v = l[r];
 #pragma unroll
       for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == (r & 31)) wmax[sw * NR + r] = v;
+      if (lane == r) wmax[sw * NR + r] = v;
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");
     if (!ok && !*abort) record_timeout(err, abort);
@@ -1269,28 +1256,22 @@ scored_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           plan.part_lse[(long)split * n_rows + prow + r] = n_tiles > 0 && sum != 0.f ? ref + log2f(sum) : -INFINITY;
         }
       }
+      float v[NR];
+      ptx::tmem_ld(o_addr, v);
+      ptx::tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < NR; c += 16) {
-        if (c < rows) {
-          float v[16];
-          ptx::tmem_ld(o_addr + c, v);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int r = c + e;
-            if (r < rows && d < HD) {
-              const float sum = wmax[r] + wmax[NR + r] + wmax[2 * NR + r] + wmax[3 * NR + r];
-              const bool seen = n_tiles > 0 && sum != 0.f;
-              const float y = seen ? v[e] / sum : 0.f;
-              if (plan.parts > 1) {
-                if (seen) plan.part_o[((long)split * n_rows + prow + r) * HD + d] = y;
-              } else {
-                const int i = r / a.G, g = r - i * a.G;
-                static_cast<bf16*>(a.out)[b * a.o_batch + i * a.o_token + (long)(hk * a.G + g) * a.o_head + d] =
-                    __float2bfloat16_rn(y);
-                if (!(fabsf(y) < INFINITY)) bad[r] = 1;
-              }
-            }
+      for (int r = 0; r < NR; ++r) {
+        if (r < rows && d < HD) {
+          const float sum = wmax[r] + wmax[NR + r] + wmax[2 * NR + r] + wmax[3 * NR + r];
+          const bool seen = n_tiles > 0 && sum != 0.f;
+          const float y = seen ? v[r] / sum : 0.f;
+          if (plan.parts > 1) {
+            if (seen) plan.part_o[((long)split * n_rows + prow + r) * HD + d] = y;
+          } else {
+            const int i = r / a.G, g = r - i * a.G;
+            static_cast<bf16*>(a.out)[b * a.o_batch + i * a.o_token + (long)(hk * a.G + g) * a.o_head + d] =
+                __float2bfloat16_rn(y);
+            if (!(fabsf(y) < INFINITY)) bad[r] = 1;
           }
         }
       }
@@ -2100,11 +2081,12 @@ cudaError_t launch_rows_kernel(const ScoredAttention& a, const ScoredPlan& plan,
 
 template <int HD, int TILES>
 cudaError_t launch_rows(const ScoredAttention& a, const ScoredPlan& plan, DevError* err, cudaStream_t st) {
-  if (a.cap > 0.f)
-    return a.slopes ? launch_rows_kernel<HD, true, true, TILES>(a, plan, err, st)
-                    : launch_rows_kernel<HD, true, false, TILES>(a, plan, err, st);
-  return a.slopes ? launch_rows_kernel<HD, false, true, TILES>(a, plan, err, st)
-                  : launch_rows_kernel<HD, false, false, TILES>(a, plan, err, st);
+  if constexpr (TILES == 1)   // the plan takes two under a cap only
+    if (!(a.cap > 0.f))
+      return a.slopes ? launch_rows_kernel<HD, false, true, 1>(a, plan, err, st)
+                      : launch_rows_kernel<HD, false, false, 1>(a, plan, err, st);
+  return a.slopes ? launch_rows_kernel<HD, true, true, TILES>(a, plan, err, st)
+                  : launch_rows_kernel<HD, true, false, TILES>(a, plan, err, st);
 }
 
 template <int HD>
