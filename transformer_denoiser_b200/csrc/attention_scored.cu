@@ -264,7 +264,7 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
 struct RowTile {
   int docs_lo, docs_hi;   // smallest and largest document of its rows (lo > hi: none)
   int any_none;           // a row in no document
-  int key_end;            // of tile 0: the keys that the CTA's rows see end here
+  int pad;
 };
 
 // Summary of a key tile's documents, its keys spread over a warp (-1: no document): x = the
@@ -370,7 +370,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   }
   ptx::pdl_wait();
   ptx::pdl_trigger();
-  const SeqInfo seq = sequence_info(a, b);
+  SeqInfo seq = sequence_info(a, b);
   __syncthreads();
 
   // ---------------- queries into shared memory (K-major, 128-byte swizzle), rows' documents
@@ -412,7 +412,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   // ---------------- key tiles of this CTA
   const int row_last = min(row0 + TILES * TILE, rows) - 1;
   const int key_end = 1 + last_key(a, seq, (long)seq.start + row_last / a.G);
-  if (threadIdx.x == 0) tiles[0].key_end = key_end;
+  seq.kv_len = key_end;   // what no row of this CTA sees counts as behind the keys
   const int jt_all = (key_end + TILE - 1) / TILE;
   const int jt0 = min(split * plan.tiles_per_split, jt_all);
   const int jt1 = plan.splits == 1 ? jt_all : min(jt0 + plan.tiles_per_split, jt_all);
@@ -622,7 +622,7 @@ scored_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             pend = true;
             v_stage = stage;
             v_phase = phase;
-            v_rows = min(tiles[0].key_end - jt * TILE, TILE);   // (shared memory: registers are short)
+            v_rows = min(seq.kv_len - jt * TILE, TILE);
           }
           unlock();
         }
