@@ -10,6 +10,15 @@ from gpu_fixtures import require_cuda
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def _fp32_default():
+    """Tensors drawn here are fp32 whatever default another module has set."""
+    was = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(was)
+
+
 def _time(call):
     """Least of seven device times (ms)."""
     best = float("inf")

@@ -8,6 +8,15 @@ from gpu_fixtures import require_cuda
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True)
+def _fp32_default():
+    """Tensors drawn here are fp32 whatever default another module has set."""
+    was = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(was)
+
 BF16, FP32 = torch.bfloat16, torch.float32
 
 

@@ -9,6 +9,15 @@ from gpu_fixtures import require_cuda
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True)
+def _fp32_default():
+    """Tensors drawn here are fp32 whatever default another module has set."""
+    was = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(was)
+
 BF16, FP32 = torch.bfloat16, torch.float32
 # B, Sq, Sk, Hq, Hkv, D: new tokens over a cache in one part and in several, prompts in one part and in several
 SHAPES = [(3, 1, 100, 8, 2, 128), (3, 2, 5000, 4, 1, 64), (3, 70, 300, 2, 1, 128), (3, 60, 2600, 2, 2, 128),

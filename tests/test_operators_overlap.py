@@ -136,7 +136,7 @@ def test_parts_of_one_buffer():
         kb.attention_scored(q, k, v, out=buf.flatten(2, 3)[:, :, 1:5])
     y = torch.randn(40, 96, generator=g, dtype=torch.float32).cuda()
     a, w = (torch.randint(-127, 128, (n, 64), generator=g, dtype=torch.int8).cuda() for n in (40, 32))
-    sa, sw = torch.ones(40, device="cuda") / 99, torch.ones(32, device="cuda") / 99
+    sa, sw = (torch.full((n,), 1 / 99, dtype=torch.float32, device="cuda") for n in (40, 32))
     kb.gemm_int8(a, sa, w, sw, None, kb.EPI_BIAS_RESID, True, y[:, :32], out=y[:, 32:64])
     assert torch.equal(y[:, 32:64], kb.gemm_int8(a, sa, w, sw, None, kb.EPI_BIAS_RESID, True, y[:, :32].clone()))
     with pytest.raises(kb.KimodoError, match="overlap"):
