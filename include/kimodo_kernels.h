@@ -166,7 +166,9 @@ KIMODO_API int kimodo_gemm_int8(const void* A, long long lda, const float* a_sca
  * Key j is seen if j < kv_lengths[b], and, with causal, j <= p_i or j < prefix[b], and, with
  * documents, q_documents[b, i] == kv_documents[b, j] >= 0 (a negative number: in no
  * document).  o_i = sum_j softmax_j(x_ij) v_j over the keys seen, 0 if there are none.
- * NaN and infinities in keys and values that a query does not see never reach its output.
+ * NaN and infinities in keys and values that a query does not see never reach its output.  Behind the
+ * last key that any query of the call sees they cost nothing; among the keys of other queries
+ * or documents they cost time (such rows are computed again, key by key).
  *
  * q, out: [batch, q_len, q_heads, head_dim]; k, v: [batch, kv_len, kv_heads, head_dim]; head
  *   h reads key head h / (q_heads / kv_heads).  head_dim 64 or 128, its elements
