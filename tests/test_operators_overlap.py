@@ -39,6 +39,9 @@ def test_quantize(lib):
     assert _quantize(lib, P, 96, P + 321, 384, 10, 64)
     assert _quantize(lib, P, 96, P + 255, 384, 10, 64)
     assert not _quantize(lib, P, 96, P + 384 * 9 + 256, 64, 1, 64)       # a row of its own behind the tenth
+    # strides whose bytes leave 64 bits: x's rows are farther apart than q is wide
+    assert not _quantize(lib, P, 2 ** 62 + 64, P + 256, 64, 2, 64)
+    assert _quantize(lib, P, 2 ** 62 + 64, P + 252, 64, 2, 64)
 
 
 def test_rms_norm(lib):

@@ -70,18 +70,18 @@ int check_type(const char* what, const void* p, int bf16_flag) {
   return KIMODO_OK;
 }
 
+using Wide = __int128;   // strides in bytes, and extents times strides, can leave 64 bits
+
 // Where a tensor lies: `width` consecutive bytes, repeated along up to three dimensions.
 struct Place {
   const void* p;
   long long width;
   long long extent[3] = {1, 1, 1};
-  long long stride[3] = {0, 0, 0};   // bytes, >= 0
+  Wide stride[3] = {0, 0, 0};   // bytes, >= 0
 };
 Place place_of_rows(const void* p, long long rows, long long cols, long long ld, int elem) {
-  return Place{p, cols * elem, {rows, 1, 1}, {ld * elem, 0, 0}};
+  return Place{p, cols * elem, {rows, 1, 1}, {(Wide)ld * elem, 0, 0}};
 }
-
-using Wide = __int128;   // extents times strides can leave 64 bits
 
 // Whether two tensors have no byte in common.  Where their ranges meet, they may still be parts of one
 // buffer (columns of the same rows, heads of the same tokens): modulo a stride of either, each
