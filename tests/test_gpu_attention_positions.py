@@ -84,3 +84,15 @@ def test_rows_computed_again_count_the_same_way(shape, dtype):
     kw = dict(slopes=_slopes(shape[3]), q_start=_i32(Sk + 10 ** 6, -10 ** 6, 0), kv_documents=d,
               q_documents=torch.ones(B, Sq, dtype=torch.int32).cuda())
     check(kb.attention_scored(q, k, v, **kw), q, k, v, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("Sq", [1, 40])
+def test_a_document_far_from_its_query(Sq, dtype):
+    """A bias is right to |slope| d 2^-20 at the distance d of the row's own document, no better."""
+    Sk = 33000
+    q, k, v = _qkv(5, 1, Sq, Sk, 4, 2, 64, dtype)
+    d = torch.full((1, Sk), 7, dtype=torch.int32)
+    d[0, 1000:1300] = 3
+    kw = dict(slopes=_slopes(4), kv_documents=d.cuda(), q_documents=torch.full((1, Sq), 3, dtype=torch.int32).cuda())
+    check(kb.attention_scored(q, k, v, **kw), q, k, v, **kw)
